@@ -17,6 +17,17 @@ struct Shape {
   const int32_t* seq_lens;
   int64_t q_s[3], k_s[3], v_s[3], qi_s[3], ki_s[2], o_s[3];
   KvPages pages;  // table == nullptr: contiguous K/V/K_idx
+  // 8-bit cache (K and V are e4m3 codes): their scales per (block, KV head),
+  // [batch, nblk, h] or [num_pages, h]
+  bool kv8;
+  const float *ks, *vs;
+};
+
+// The tensors of an 8-bit cache: e4m3 codes with the shape's strides, and fp32
+// scales, dense [batch, nblk, h] or [num_pages, h] (K_idx: without the head axis).
+struct Q8Cache {
+  uint8_t *k, *v, *ki;
+  float *ks, *vs, *kis;
 };
 
 // Stage 1a/1b: block-max-pooled index scores, fp32 [batch, n_q, h, nblk].
@@ -75,6 +86,22 @@ cudaError_t launch_append_kv(const Shape& s, const uint16_t* k_new, const uint16
                              const uint16_t* ki_new, uint16_t* k, uint16_t* v, uint16_t* ki,
                              DeviceStatus* st, cudaStream_t stream);
 
+// The same write into an 8-bit cache (kv_q8.cu).
+cudaError_t launch_append_kv_q8(const Shape& s, const uint16_t* k_new, const uint16_t* v_new,
+                                const uint16_t* ki_new, const Q8Cache& c, DeviceStatus* st,
+                                cudaStream_t stream);
+
+// Rows [base, base + n) of every sequence of an 8-bit cache (those below its length)
+// as bf16, dense [batch, n, h, d] / [batch, n, d_idx].
+cudaError_t launch_read_kv_q8(const Shape& s, const Q8Cache& c, int64_t base, int64_t n,
+                              uint16_t* k_out, uint16_t* v_out, uint16_t* ki_out, DeviceStatus* st,
+                              cudaStream_t stream);
+
+// Stage 1a/1b over an 8-bit index key, one query per sequence (index_scores_q8.cu).
+cudaError_t launch_index_scan_q8(const Shape& s, const uint16_t* q_idx, const uint8_t* k_idx,
+                                 const float* k_idx_scale, float* scores, bool fill_tail,
+                                 DeviceStatus* st, cudaStream_t stream);
+
 // Stage 2: workspace bytes for the split-KV partials, then the attention.
 size_t attn_partial_bytes(const Shape& s);
 int attn_launches(const Shape& s);
@@ -86,8 +113,9 @@ int* attn_merge_counters(const Shape& s, void* partials, int* count);
 // `partials`, cleared by a memset unless `counters_zeroed` (the top-k kernel of
 // the same forward cleared them already).  The kernel puts every counter it uses
 // back to zero.
-cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const uint16_t* k,
-                               const uint16_t* v, const int32_t* ids, uint16_t* out, float* lse,
+// With s.kv8 set, k and v are e4m3 codes.
+cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const void* k,
+                               const void* v, const int32_t* ids, uint16_t* out, float* lse,
                                void* partials, size_t partial_bytes, DeviceStatus* st,
                                cudaStream_t stream, bool counters_zeroed = false,
                                int* fixed_counters = nullptr);

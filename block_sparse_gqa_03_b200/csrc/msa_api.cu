@@ -131,6 +131,8 @@ msa_status_t make_shape(const msa_params_t* p, Shape* s) {
   s->pages.table = p->block_table;
   s->pages.stride = p->table_stride;
   s->pages.pages = p->num_pages;
+  s->kv8 = false;
+  s->ks = s->vs = nullptr;
   if (p->block_table != nullptr) {
     // one page per block; page coordinates are int32 in the tensor maps
     if ((reinterpret_cast<uintptr_t>(p->block_table) & 3u) != 0 || p->table_stride < nblk ||
@@ -167,6 +169,47 @@ msa_status_t check_attn_args(const Shape& s, const void* q, const void* k, const
   return MSA_OK;
 }
 
+// ---- 8-bit cache: rows of one-byte codes, 16-byte aligned; fp32 scales
+bool good_stride16(int64_t st) { return st > 0 && (st % 16) == 0; }
+
+bool good_codes(const void* codes, const float* scale, const int64_t* st, int d) {
+  return codes != nullptr && scale != nullptr && aligned16(codes) &&
+         (reinterpret_cast<uintptr_t>(scale) & 3u) == 0 && good_stride16(st[0]) &&
+         good_stride16(st[1]) && good_stride16(st[2]) && st[2] >= d;
+}
+
+bool good_idx_codes(const Shape& s, const void* codes, const float* scale) {
+  return codes != nullptr && scale != nullptr && aligned16(codes) &&
+         (reinterpret_cast<uintptr_t>(scale) & 3u) == 0 && good_stride16(s.ki_s[0]) &&
+         good_stride16(s.ki_s[1]) && s.ki_s[1] >= s.d_idx;
+}
+
+msa_status_t check_select_args_q8(const Shape& s, const void* q_idx, const void* k_idx,
+                                  const float* scale) {
+  if (!q_idx || !aligned16(q_idx) || check_strides3(s.qi_s) != MSA_OK || s.qi_s[2] < s.d_idx ||
+      !good_idx_codes(s, k_idx, scale))
+    return MSA_ERR_INVALID_ARG;
+  return MSA_OK;
+}
+
+msa_status_t check_attn_args_q8(const Shape& s, const void* q, const void* k, const void* v,
+                                const float* ks, const float* vs, const void* out) {
+  if (!q || !out || !aligned16(q) || !aligned16(out) || check_strides3(s.q_s) != MSA_OK ||
+      check_strides3(s.o_s) != MSA_OK || s.q_s[2] < s.d || s.o_s[2] < s.d ||
+      !good_codes(k, ks, s.k_s, s.d) || !good_codes(v, vs, s.v_s, s.d))
+    return MSA_ERR_INVALID_ARG;
+  return MSA_OK;
+}
+
+bool q8_op(msa_op_t op) { return op >= MSA_OP_APPEND_KV_Q8 && op <= MSA_OP_FORWARD_Q8; }
+
+// Prefill scores over an 8-bit index key run the bf16 index kernels on a widened
+// copy of the key, which costs 5 bytes per key element against the 2 d_idx n_q h
+// operations that each element enters.
+size_t wide_idx_bytes(const Shape& s) {
+  return s.n_q > 1 ? (size_t)s.batch * s.max_kv * s.d_idx * 2 : 0;
+}
+
 size_t scores_bytes(const Shape& s) {
   return (size_t)s.batch * s.n_q * s.h * s.nblk * sizeof(float);
 }
@@ -177,24 +220,31 @@ size_t ids_bytes(const Shape& s) {
 
 // Workspace layout: [status region (status word, decode merge counters) | scores |
 // ids | attention partials], 256-aligned parts.
+// The 8-bit index operations put the widened index key in front of the scores.
 struct Layout {
-  size_t scores_off, ids_off, part_off, part_bytes, total;
+  size_t wide_off, scores_off, ids_off, part_off, part_bytes, total;
 };
 
 Layout layout(const Shape& s, msa_op_t op) {
   Layout l;
   size_t off = msa::kStatusBytes;
-  l.scores_off = l.ids_off = l.part_off = 0;
+  l.wide_off = l.scores_off = l.ids_off = l.part_off = 0;
   l.part_bytes = 0;
-  if (op == MSA_OP_INDEX_SELECT || op == MSA_OP_INDEX_CANDIDATES || op == MSA_OP_FORWARD) {
+  if (op == MSA_OP_BLOCK_SCORES_Q8 || op == MSA_OP_INDEX_SELECT_Q8 || op == MSA_OP_FORWARD_Q8) {
+    l.wide_off = off;
+    off = align_up(off + wide_idx_bytes(s));
+  }
+  if (op == MSA_OP_INDEX_SELECT || op == MSA_OP_INDEX_CANDIDATES || op == MSA_OP_FORWARD ||
+      op == MSA_OP_INDEX_SELECT_Q8 || op == MSA_OP_FORWARD_Q8) {
     l.scores_off = off;
     off = align_up(off + scores_bytes(s));
   }
-  if (op == MSA_OP_FORWARD) {
+  if (op == MSA_OP_FORWARD || op == MSA_OP_FORWARD_Q8) {
     l.ids_off = off;
     off = align_up(off + ids_bytes(s));
   }
-  if (op == MSA_OP_SPARSE_ATTN || op == MSA_OP_FORWARD) {
+  if (op == MSA_OP_SPARSE_ATTN || op == MSA_OP_FORWARD || op == MSA_OP_SPARSE_ATTN_Q8 ||
+      op == MSA_OP_FORWARD_Q8) {
     l.part_bytes = msa::attn_partial_bytes(s);
     l.part_off = off;
     off = align_up(off + l.part_bytes);
@@ -206,7 +256,8 @@ Layout layout(const Shape& s, msa_op_t op) {
 // Operations whose workspace holds the status word only.
 bool status_only(msa_op_t op) {
   return op == MSA_OP_APPEND_KV || op == MSA_OP_BLOCK_SCORES || op == MSA_OP_SELECT_CANDIDATES ||
-         op == MSA_OP_SHARD_LENGTHS || op == MSA_OP_INDEX_TOPK;
+         op == MSA_OP_SHARD_LENGTHS || op == MSA_OP_INDEX_TOPK || op == MSA_OP_APPEND_KV_Q8 ||
+         op == MSA_OP_READ_KV_Q8;
 }
 
 msa_status_t check_ws(const Shape& s, msa_op_t op, void* ws, size_t bytes) {
@@ -251,8 +302,9 @@ size_t msa_workspace_size(const msa_params_t* params, msa_op_t op) {
   Shape s;
   if (make_shape(params, &s) != MSA_OK) return 0;
   if (status_only(op)) return msa::kStatusBytes;
+  s.kv8 = q8_op(op);
   if (op != MSA_OP_INDEX_SELECT && op != MSA_OP_SPARSE_ATTN && op != MSA_OP_FORWARD &&
-      op != MSA_OP_INDEX_CANDIDATES)
+      op != MSA_OP_INDEX_CANDIDATES && !s.kv8)
     return 0;
   return layout(s, op).total;
 }
@@ -481,6 +533,14 @@ int msa_launch_count(const msa_params_t* params, msa_op_t op) {
     case MSA_OP_SELECT_CANDIDATES: return 1;
     case MSA_OP_SHARD_LENGTHS: return 1;
     case MSA_OP_INDEX_TOPK: return 1;
+    case MSA_OP_APPEND_KV_Q8: return 1;
+    case MSA_OP_READ_KV_Q8: return 1;
+    case MSA_OP_BLOCK_SCORES_Q8: return s.n_q > 1 ? 2 : 1;
+    case MSA_OP_INDEX_SELECT_Q8: return s.n_q > 1 ? 3 : 2;
+    case MSA_OP_SPARSE_ATTN_Q8: s.kv8 = true; return msa::attn_launches(s);
+    case MSA_OP_FORWARD_Q8:
+      s.kv8 = true;
+      return (s.n_q > 1 ? 3 : 2) + msa::attn_launches(s);
   }
   return -1;
 }
@@ -496,6 +556,170 @@ const char* msa_status_string(msa_status_t status) {
     case MSA_ERR_DEVICE_ASSERT: return "device-side precondition failed";
   }
   return "unknown status";
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// 8-bit cache
+namespace {
+
+cudaError_t run_scores_q8(const Shape& s, const msa_bf16_t* q_idx, const uint8_t* k_idx,
+                          const float* k_idx_scale, float* scores, bool fill_tail, void* ws,
+                          const Layout& l, cudaStream_t stream) {
+  msa::DeviceStatus* st = reinterpret_cast<msa::DeviceStatus*>(ws);
+  if (s.n_q == 1)
+    return msa::launch_index_scan_q8(s, q_idx, k_idx, k_idx_scale, scores, fill_tail, st, stream);
+  uint16_t* wide = reinterpret_cast<uint16_t*>(at(ws, l.wide_off));
+  msa::Q8Cache c = {};
+  c.ki = const_cast<uint8_t*>(k_idx);
+  c.kis = const_cast<float*>(k_idx_scale);
+  const cudaError_t e = msa::launch_read_kv_q8(s, c, 0, s.max_kv, nullptr, nullptr, wide, st, stream);
+  if (e != cudaSuccess) return e;
+  Shape w = s;  // the widened key is dense, one row per token
+  w.pages.table = nullptr;
+  w.ki_s[0] = (int64_t)s.max_kv * s.d_idx;
+  w.ki_s[1] = s.d_idx;
+  return run_scores(w, q_idx, wide, scores, fill_tail, st, stream);
+}
+
+msa_status_t run_select_q8(const Shape& s, const msa_bf16_t* q_idx, const uint8_t* k_idx,
+                           const float* k_idx_scale, int32_t* ids, float* user_scores, void* ws,
+                           const Layout& l, cudaStream_t stream, int* zero = nullptr,
+                           int nzero = 0) {
+  float* scores = user_scores ? user_scores : reinterpret_cast<float*>(at(ws, l.scores_off));
+  if (run_scores_q8(s, q_idx, k_idx, k_idx_scale, scores, user_scores != nullptr, ws, l, stream) !=
+      cudaSuccess)
+    return MSA_ERR_CUDA;
+  return cuda_status(msa::launch_topk(s, scores, ids, reinterpret_cast<msa::DeviceStatus*>(ws),
+                                      stream, zero, nzero));
+}
+
+}  // namespace
+
+extern "C" {
+
+msa_status_t msa_append_kv_q8(const msa_params_t* params, const msa_bf16_t* k_new,
+                              const msa_bf16_t* v_new, const msa_bf16_t* k_idx_new,
+                              msa_e4m3_t* k, msa_e4m3_t* v, msa_e4m3_t* k_idx, float* k_scale,
+                              float* v_scale, float* k_idx_scale, void* workspace,
+                              size_t workspace_bytes, msa_stream_t stream) {
+  Shape s;
+  msa_status_t rc = make_shape(params, &s);
+  if (rc != MSA_OK) return rc;
+  if (!k_new && !v_new && !k_idx_new) return MSA_ERR_INVALID_ARG;
+  if ((k_new && (!aligned16(k_new) || !good_codes(k, k_scale, s.k_s, s.d))) ||
+      (v_new && (!aligned16(v_new) || !good_codes(v, v_scale, s.v_s, s.d))) ||
+      (k_idx_new && (!aligned16(k_idx_new) || !good_idx_codes(s, k_idx, k_idx_scale))))
+    return MSA_ERR_INVALID_ARG;
+  if ((rc = check_ws(s, MSA_OP_APPEND_KV_Q8, workspace, workspace_bytes)) != MSA_OK) return rc;
+  const msa::Q8Cache c = {k, v, k_idx, k_scale, v_scale, k_idx_scale};
+  return cuda_status(msa::launch_append_kv_q8(s, k_new, v_new, k_idx_new, c,
+                                              reinterpret_cast<msa::DeviceStatus*>(workspace),
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status_t msa_read_kv_q8(const msa_params_t* params, const msa_e4m3_t* k, const msa_e4m3_t* v,
+                            const msa_e4m3_t* k_idx, const float* k_scale, const float* v_scale,
+                            const float* k_idx_scale, int64_t token_base, msa_bf16_t* k_out,
+                            msa_bf16_t* v_out, msa_bf16_t* k_idx_out, void* workspace,
+                            size_t workspace_bytes, msa_stream_t stream) {
+  Shape s;
+  msa_status_t rc = make_shape(params, &s);
+  if (rc != MSA_OK) return rc;
+  if (token_base < 0 || token_base + s.n_q > s.max_kv || (!k_out && !v_out && !k_idx_out))
+    return MSA_ERR_INVALID_ARG;
+  if ((k_out && (!aligned16(k_out) || !good_codes(k, k_scale, s.k_s, s.d))) ||
+      (v_out && (!aligned16(v_out) || !good_codes(v, v_scale, s.v_s, s.d))) ||
+      (k_idx_out && (!aligned16(k_idx_out) || !good_idx_codes(s, k_idx, k_idx_scale))))
+    return MSA_ERR_INVALID_ARG;
+  if ((rc = check_ws(s, MSA_OP_READ_KV_Q8, workspace, workspace_bytes)) != MSA_OK) return rc;
+  const msa::Q8Cache c = {const_cast<msa_e4m3_t*>(k),     const_cast<msa_e4m3_t*>(v),
+                          const_cast<msa_e4m3_t*>(k_idx), const_cast<float*>(k_scale),
+                          const_cast<float*>(v_scale),    const_cast<float*>(k_idx_scale)};
+  return cuda_status(msa::launch_read_kv_q8(s, c, token_base, s.n_q, k_out, v_out, k_idx_out,
+                                            reinterpret_cast<msa::DeviceStatus*>(workspace),
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status_t msa_block_scores_q8(const msa_params_t* params, const msa_bf16_t* q_idx,
+                                 const msa_e4m3_t* k_idx, const float* k_idx_scale,
+                                 float* block_scores, void* workspace, size_t workspace_bytes,
+                                 msa_stream_t stream) {
+  Shape s;
+  msa_status_t rc = make_shape(params, &s);
+  if (rc != MSA_OK) return rc;
+  if ((rc = check_select_args_q8(s, q_idx, k_idx, k_idx_scale)) != MSA_OK) return rc;
+  if (block_scores == nullptr) return MSA_ERR_INVALID_ARG;
+  if ((rc = check_ws(s, MSA_OP_BLOCK_SCORES_Q8, workspace, workspace_bytes)) != MSA_OK) return rc;
+  return cuda_status(run_scores_q8(s, q_idx, k_idx, k_idx_scale, block_scores, true, workspace,
+                                   layout(s, MSA_OP_BLOCK_SCORES_Q8),
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status_t msa_index_select_q8(const msa_params_t* params, const msa_bf16_t* q_idx,
+                                 const msa_e4m3_t* k_idx, const float* k_idx_scale,
+                                 int32_t* block_ids, float* block_scores, void* workspace,
+                                 size_t workspace_bytes, msa_stream_t stream) {
+  Shape s;
+  msa_status_t rc = make_shape(params, &s);
+  if (rc != MSA_OK) return rc;
+  if ((rc = check_select_args_q8(s, q_idx, k_idx, k_idx_scale)) != MSA_OK) return rc;
+  if (block_ids == nullptr) return MSA_ERR_INVALID_ARG;
+  if ((rc = check_ws(s, MSA_OP_INDEX_SELECT_Q8, workspace, workspace_bytes)) != MSA_OK) return rc;
+  return run_select_q8(s, q_idx, k_idx, k_idx_scale, block_ids, block_scores, workspace,
+                       layout(s, MSA_OP_INDEX_SELECT_Q8), reinterpret_cast<cudaStream_t>(stream));
+}
+
+msa_status_t msa_sparse_attn_q8(const msa_params_t* params, const msa_bf16_t* q,
+                                const msa_e4m3_t* k, const msa_e4m3_t* v, const float* k_scale,
+                                const float* v_scale, const int32_t* block_ids, msa_bf16_t* out,
+                                float* lse, void* workspace, size_t workspace_bytes,
+                                msa_stream_t stream) {
+  Shape s;
+  msa_status_t rc = make_shape(params, &s);
+  if (rc != MSA_OK) return rc;
+  if ((rc = check_attn_args_q8(s, q, k, v, k_scale, v_scale, out)) != MSA_OK) return rc;
+  if (block_ids == nullptr) return MSA_ERR_INVALID_ARG;
+  s.kv8 = true;
+  s.ks = k_scale;
+  s.vs = v_scale;
+  if ((rc = check_ws(s, MSA_OP_SPARSE_ATTN_Q8, workspace, workspace_bytes)) != MSA_OK) return rc;
+  const Layout l = layout(s, MSA_OP_SPARSE_ATTN_Q8);
+  return cuda_status(msa::launch_sparse_attn(
+      s, q, k, v, block_ids, out, lse, at(workspace, l.part_off), l.part_bytes,
+      reinterpret_cast<msa::DeviceStatus*>(workspace), reinterpret_cast<cudaStream_t>(stream),
+      false, fixed_counters(workspace)));
+}
+
+msa_status_t msa_forward_q8(const msa_params_t* params, const msa_bf16_t* q, const msa_e4m3_t* k,
+                            const msa_e4m3_t* v, const msa_bf16_t* q_idx, const msa_e4m3_t* k_idx,
+                            const float* k_scale, const float* v_scale, const float* k_idx_scale,
+                            msa_bf16_t* out, int32_t* block_ids, float* block_scores, float* lse,
+                            void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  Shape s;
+  msa_status_t rc = make_shape(params, &s);
+  if (rc != MSA_OK) return rc;
+  if ((rc = check_select_args_q8(s, q_idx, k_idx, k_idx_scale)) != MSA_OK) return rc;
+  if ((rc = check_attn_args_q8(s, q, k, v, k_scale, v_scale, out)) != MSA_OK) return rc;
+  s.kv8 = true;
+  s.ks = k_scale;
+  s.vs = v_scale;
+  if ((rc = check_ws(s, MSA_OP_FORWARD_Q8, workspace, workspace_bytes)) != MSA_OK) return rc;
+  const Layout l = layout(s, MSA_OP_FORWARD_Q8);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  int32_t* ids = block_ids ? block_ids : reinterpret_cast<int32_t*>(at(workspace, l.ids_off));
+  // merge counters as in msa_forward
+  int ncounters = 0;
+  int* counters = msa::attn_merge_counters(s, at(workspace, l.part_off), &ncounters);
+  if (counters != nullptr && ncounters <= msa::kFixedCounters) counters = nullptr;
+  if ((rc = run_select_q8(s, q_idx, k_idx, k_idx_scale, ids, block_scores, workspace, l, cs,
+                          counters, ncounters)) != MSA_OK)
+    return rc;
+  return cuda_status(msa::launch_sparse_attn(s, q, k, v, ids, out, lse, at(workspace, l.part_off),
+                                             l.part_bytes,
+                                             reinterpret_cast<msa::DeviceStatus*>(workspace), cs,
+                                             counters != nullptr, fixed_counters(workspace)));
 }
 
 }  // extern "C"

@@ -31,7 +31,14 @@
 // back to zero by the merging CTA) merges them by log-sum-exp weights.  The row's first CTA, which reaches the
 // row at the end of its range, usually finds the others' partials already
 // published and merges them into its own state without writing its own.
+//
+// 8-bit cache (e4m3 codes, a scale per (block, KV head)): the same two kernels with
+// the Q8 warp states below.  A stage holds half the bytes (rows of d bytes, one TMA
+// box per tile), codes are widened to f16 between ldmatrix and the MMA, a block's K
+// scale joins the softmax scale of its scores and its V scale the fp32 accumulation
+// of its product, so that neither is ever rounded to 16 bits.
 #include "kernels.h"
+#include "q8.cuh"
 
 namespace msa {
 namespace {
@@ -58,6 +65,7 @@ struct AttnArgs {
   DeviceStatus* st;
   uint64_t wait_ns;
   KvPages pg;  // table == nullptr: contiguous K/V
+  const float *ks, *vs;  // 8-bit cache: scales per (block, KV head)
 };
 
 constexpr float kLn2 = 0.69314718055994531f;
@@ -89,6 +97,7 @@ __device__ __forceinline__ RowGeo row_geo(const AttnArgs& a, int64_t rowg) {
 // Running softmax state of one warp: rows r and r + 8 of the 16-row tile.
 template <int D>
 struct WarpState {
+  static constexpr bool kQ8 = false;
   uint32_t qa[D / 16][4];
   float o[D / 8][4];
   float m_a, m_b, l_a, l_b;
@@ -245,6 +254,7 @@ struct WarpState {
 // its own part of the running sum.
 template <int D>
 struct WarpStateT {
+  static constexpr bool kQ8 = false;
   uint32_t qb[D / 16][2];  // B fragments of Q^T: dims 16kk + 2 (lane % 4) (+8), head lane / 4
   float o[D / 16][4];      // O^T tile mt: dims 16mt + lane / 4 (+8), heads 2 (lane % 4) (+1)
   float m0, m1, l0, l1;
@@ -374,6 +384,300 @@ struct WarpStateT {
   }
 };
 
+// ------------------------------------------------------------- 8-bit cache
+// Zeroes V rows [r0, 16) of a 16-token slice at row `tok` (codes that may be
+// uninitialised memory: a NaN code must not meet a zero probability).
+template <int D>
+__device__ __forceinline__ void zero_v_rows(uint8_t* vtile, int tok, int r0, int lane) {
+  constexpr int CPR = D / 16;  // 16-byte pieces per row; the swizzle stays inside a row
+  for (int x = lane; x < (16 - r0) * CPR; x += 32)
+    reinterpret_cast<uint4*>(vtile + (tok + r0) * D)[x] = make_uint4(0, 0, 0, 0);
+}
+
+// Four transposed codes (two tokens x two neighbouring dims, as ldmatrix.trans
+// leaves them) regrouped by dim: low half the even dim's two tokens.
+__device__ __forceinline__ uint32_t by_dim(uint32_t v) { return __byte_perm(v, 0, 0x3120); }
+
+// WarpStateT over an 8-bit cache: groups of at most 8 heads, operands swapped.  A
+// K register holds four consecutive dims of a token, so k-step c takes its 16 dims
+// in the order 4j, 4j + 1, 4j + 2, 4j + 3 per lane quad j and the query fragments
+// follow it; a transposed V register holds two dims of two tokens, so output row r
+// of tile mt is dim 16mt + 2r and row r + 8 dim 16mt + 2r + 1.
+template <int D>
+struct WarpStateTQ {
+  static constexpr bool kQ8 = true;
+  uint32_t qlo[D / 16], qhi[D / 16];
+  float o[D / 16][4];
+  float m0, m1, l0, l1;
+  float f0, f1;  // softmax scale (log2) with the query scaling undone, heads 2q4, 2q4 + 1
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m0 = m1 = neg_inf();
+    l0 = l1 = 0.f;
+  }
+
+  __device__ __forceinline__ void load_q(const AttnArgs& a, const RowGeo& rg, int lane) {
+    const int r = lane >> 2, q4 = lane & 3;
+    const float inv = q8::load_row_f16<D / 16>(a.q + rg.b * a.q_s0 + (int64_t)rg.t * a.q_s1 +
+                                                   (int64_t)(rg.g * a.G + r) * a.q_s2 + 4 * q4,
+                                               r < a.G, qlo, qhi) *
+                      a.scale_log2;
+    f0 = __shfl_sync(0xffffffffu, inv, 8 * q4);
+    f1 = __shfl_sync(0xffffffffu, inv, 8 * q4 + 4);
+  }
+
+  __device__ __forceinline__ void attend(uint8_t* smem, uint32_t sbase, uint32_t kbase,
+                                         uint32_t vbase, int tok, int j0, int lim, int lane,
+                                         float ks, float vs, bool& wrote_smem) {
+    const int r = lane >> 2;
+    const float ninf = neg_inf();
+    if (j0 + 16 > lim) {
+      zero_v_rows<D>(smem + (vbase - sbase), tok, lim - j0, lane);
+      wrote_smem = true;
+      __syncwarp();
+    }
+    // tokens tok + lane % 16, chunks c (lanes 0-15) and c + 1
+    const uint32_t row = tok + (lane & 15);
+    // S^T: tokens tok + r (s[0], s[1]) and tok + r + 8 (s[2], s[3]), heads 2q4, 2q4 + 1;
+    // two accumulators halve the chain of dependent MMAs
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2) {
+      uint32_t k0, k1, k2, k3;  // tokens 0-7, 8-15 of step c, then of step c + 1
+      ldmatrix_x4(kbase + q8::swz<D>(row, c + (lane >> 4)), k0, k1, k2, k3);
+      q8::mma_f16(s, q8::lo_f16x2(k0), q8::lo_f16x2(k1), q8::hi_f16x2(k0), q8::hi_f16x2(k1),
+                  qlo[c], qhi[c]);
+      q8::mma_f16(t, q8::lo_f16x2(k2), q8::lo_f16x2(k3), q8::hi_f16x2(k2), q8::hi_f16x2(k3),
+                  qlo[c + 1], qhi[c + 1]);
+    }
+    const float g0 = f0 * ks, g1 = f1 * ks;
+    const bool ok_lo = j0 + r < lim, ok_hi = j0 + r + 8 < lim;
+    s[0] = ok_lo ? (s[0] + t[0]) * g0 : ninf;
+    s[1] = ok_lo ? (s[1] + t[1]) * g1 : ninf;
+    s[2] = ok_hi ? (s[2] + t[2]) * g0 : ninf;
+    s[3] = ok_hi ? (s[3] + t[3]) * g1 : ninf;
+    float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+    mx0 = warp_max_xor(warp_max_xor(warp_max_xor(mx0, 4), 8), 16);
+    mx1 = warp_max_xor(warp_max_xor(warp_max_xor(mx1, 4), 8), 16);
+    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+    const float c0 = exp2f(m0 - mn0), c1 = exp2f(m1 - mn1);
+    m0 = mn0;
+    m1 = mn1;
+    s[0] = exp2f(s[0] - mn0);
+    s[1] = exp2f(s[1] - mn1);
+    s[2] = exp2f(s[2] - mn0);
+    s[3] = exp2f(s[3] - mn1);
+    l0 = l0 * c0 + (s[0] + s[2]);
+    l1 = l1 * c1 + (s[1] + s[3]);
+    // probabilities in [0, 1] as f16 (relative error 2^-12, absolute 2^-25 below 2^-14)
+    const uint32_t pb0 = movmatrix_trans(q8::pack_f16(s[0], s[1]));
+    const uint32_t pb1 = movmatrix_trans(q8::pack_f16(s[2], s[3]));
+#pragma unroll
+    for (int mt = 0; mt < D / 16; mt += 2) {
+      uint32_t v0, v1, v2, v3;  // tokens 0-7, 8-15 of dims 16mt.., then of the next 16
+      ldmatrix_x4_trans(vbase + q8::swz<D>(row, mt + (lane >> 4)), v0, v1, v2, v3);
+      v0 = by_dim(v0);
+      v1 = by_dim(v1);
+      v2 = by_dim(v2);
+      v3 = by_dim(v3);
+      float x[4], y[4];
+      q8::mma_f16_zero(x, q8::lo_f16x2(v0), q8::hi_f16x2(v0), q8::lo_f16x2(v1), q8::hi_f16x2(v1),
+                       pb0, pb1);
+      q8::mma_f16_zero(y, q8::lo_f16x2(v2), q8::hi_f16x2(v2), q8::lo_f16x2(v3), q8::hi_f16x2(v3),
+                       pb0, pb1);
+      // o = o c + vs x
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float* p = &o[mt][e];
+        mul2(p[0], p[1], p[0], p[1], c0, c1);
+        fma2(p[0], p[1], x[e], x[e + 1], vs, vs, p[0], p[1]);
+        p = &o[mt + 1][e];
+        mul2(p[0], p[1], p[0], p[1], c0, c1);
+        fma2(p[0], p[1], y[e], y[e + 1], vs, vs, p[0], p[1]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void stash(float* mo, float* mm, float* ml, int warp, int lane,
+                                        int gr) {
+    const int r = lane >> 2, h0 = 2 * (lane & 3), h1 = h0 + 1;
+    float s0 = l0, s1 = l1;
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      s0 += __shfl_xor_sync(0xffffffffu, s0, x);
+      s1 += __shfl_xor_sync(0xffffffffu, s1, x);
+    }
+    float* mw = mo + warp * gr * D;
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) {
+      const int dd = mt * 16 + 2 * r;
+      if (h0 < gr) *reinterpret_cast<float2*>(mw + h0 * D + dd) = make_float2(o[mt][0], o[mt][2]);
+      if (h1 < gr) *reinterpret_cast<float2*>(mw + h1 * D + dd) = make_float2(o[mt][1], o[mt][3]);
+    }
+    if (r == 0) {
+      mm[warp * 16 + h0] = m0;
+      mm[warp * 16 + h1] = m1;
+      ml[warp * 16 + h0] = s0;
+      ml[warp * 16 + h1] = s1;
+    }
+  }
+};
+
+// WarpState over an 8-bit cache (up to 16 heads on the MMA rows).  Output tile
+// columns: for dims 16c .. 16c + 15, o[2c] holds the even dims and o[2c + 1] the odd
+// ones (column n is dim 16c + 2n (+ 1)).
+template <int D>
+struct WarpStateQ {
+  static constexpr bool kQ8 = true;
+  uint32_t qlo[2][D / 16], qhi[2][D / 16];  // head rows r and r + 8
+  float o[D / 8][4];
+  float m_a, m_b, l_a, l_b;
+  float f_a, f_b;  // softmax scale (log2) with the query scaling undone
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m_a = m_b = neg_inf();
+    l_a = l_b = 0.f;
+  }
+
+  __device__ __forceinline__ void load_q(const AttnArgs& a, const RowGeo& rg, int lane) {
+    const int r = lane >> 2, q4 = lane & 3;
+    const uint16_t* qb = a.q + rg.b * a.q_s0 + (int64_t)rg.t * a.q_s1 +
+                         (int64_t)(rg.g * a.G) * a.q_s2 + 4 * q4;
+    f_a = a.scale_log2 *
+          q8::load_row_f16<D / 16>(qb + (int64_t)r * a.q_s2, r < a.G, qlo[0], qhi[0]);
+    f_b = a.scale_log2 *
+          q8::load_row_f16<D / 16>(qb + (int64_t)(r + 8) * a.q_s2, r + 8 < a.G, qlo[1], qhi[1]);
+  }
+
+  __device__ __forceinline__ void attend(uint8_t* smem, uint32_t sbase, uint32_t kbase,
+                                         uint32_t vbase, int tok, int j0, int lim, int lane,
+                                         float ks, float vs, bool& wrote_smem) {
+    const int q4 = lane & 3;
+    const float ninf = neg_inf();
+    if (j0 + 16 > lim) {
+      zero_v_rows<D>(smem + (vbase - sbase), tok, lim - j0, lane);
+      wrote_smem = true;
+      __syncwarp();
+    }
+    const uint32_t row = tok + (lane & 15);
+    float sc[2][4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2) {
+      uint32_t k0, k1, k2, k3;  // tokens 0-7, 8-15 of step c, then of step c + 1
+      ldmatrix_x4(kbase + q8::swz<D>(row, c + (lane >> 4)), k0, k1, k2, k3);
+      q8::mma_f16(sc[0], qlo[0][c], qlo[1][c], qhi[0][c], qhi[1][c], q8::lo_f16x2(k0),
+                  q8::hi_f16x2(k0));
+      q8::mma_f16(sc[1], qlo[0][c], qlo[1][c], qhi[0][c], qhi[1][c], q8::lo_f16x2(k1),
+                  q8::hi_f16x2(k1));
+      q8::mma_f16(sc[0], qlo[0][c + 1], qlo[1][c + 1], qhi[0][c + 1], qhi[1][c + 1],
+                  q8::lo_f16x2(k2), q8::hi_f16x2(k2));
+      q8::mma_f16(sc[1], qlo[0][c + 1], qlo[1][c + 1], qhi[0][c + 1], qhi[1][c + 1],
+                  q8::lo_f16x2(k3), q8::hi_f16x2(k3));
+    }
+    const float g_a = f_a * ks, g_b = f_b * ks;
+    float mx_a = ninf, mx_b = ninf;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool ok = j0 + nt * 8 + 2 * q4 + e < lim;
+        sc[nt][e] = ok ? sc[nt][e] * g_a : ninf;
+        sc[nt][2 + e] = ok ? sc[nt][2 + e] * g_b : ninf;
+        mx_a = fmaxf(mx_a, sc[nt][e]);
+        mx_b = fmaxf(mx_b, sc[nt][2 + e]);
+      }
+    mx_a = warp_max_xor(warp_max_xor(mx_a, 1), 2);
+    mx_b = warp_max_xor(warp_max_xor(mx_b, 1), 2);
+    const float mn_a = fmaxf(m_a, mx_a), mn_b = fmaxf(m_b, mx_b);
+    const float c_a = exp2f(m_a - mn_a), c_b = exp2f(m_b - mn_b);
+    m_a = mn_a;
+    m_b = mn_b;
+    float ps_a = 0.f, ps_b = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sc[nt][e] = exp2f(sc[nt][e] - mn_a);
+        sc[nt][2 + e] = exp2f(sc[nt][2 + e] - mn_b);
+        ps_a += sc[nt][e];
+        ps_b += sc[nt][2 + e];
+      }
+    l_a = l_a * c_a + ps_a;
+    l_b = l_b * c_b + ps_b;
+    const uint32_t pa0 = q8::pack_f16(sc[0][0], sc[0][1]);
+    const uint32_t pa1 = q8::pack_f16(sc[0][2], sc[0][3]);
+    const uint32_t pa2 = q8::pack_f16(sc[1][0], sc[1][1]);
+    const uint32_t pa3 = q8::pack_f16(sc[1][2], sc[1][3]);
+    auto add = [&](float (&acc)[4], const float (&x)[4]) {
+      acc[0] = fmaf(vs, x[0], acc[0] * c_a);
+      acc[1] = fmaf(vs, x[1], acc[1] * c_a);
+      acc[2] = fmaf(vs, x[2], acc[2] * c_b);
+      acc[3] = fmaf(vs, x[3], acc[3] * c_b);
+    };
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2) {
+      uint32_t v0, v1, v2, v3;  // tokens 0-7, 8-15 of dims 16c.., then of the next 16
+      ldmatrix_x4_trans(vbase + q8::swz<D>(row, c + (lane >> 4)), v0, v1, v2, v3);
+      v0 = by_dim(v0);
+      v1 = by_dim(v1);
+      v2 = by_dim(v2);
+      v3 = by_dim(v3);
+      float x[4];
+      q8::mma_f16_zero(x, pa0, pa1, pa2, pa3, q8::lo_f16x2(v0), q8::lo_f16x2(v1));
+      add(o[2 * c], x);
+      q8::mma_f16_zero(x, pa0, pa1, pa2, pa3, q8::hi_f16x2(v0), q8::hi_f16x2(v1));
+      add(o[2 * c + 1], x);
+      q8::mma_f16_zero(x, pa0, pa1, pa2, pa3, q8::lo_f16x2(v2), q8::lo_f16x2(v3));
+      add(o[2 * c + 2], x);
+      q8::mma_f16_zero(x, pa0, pa1, pa2, pa3, q8::hi_f16x2(v2), q8::hi_f16x2(v3));
+      add(o[2 * c + 3], x);
+    }
+  }
+
+  __device__ __forceinline__ void stash(float* mo, float* mm, float* ml, int warp, int lane,
+                                        int gr) {
+    const int r = lane >> 2, q4 = lane & 3;
+    float la = l_a, lb = l_b;
+    la += __shfl_xor_sync(0xffffffffu, la, 1);
+    la += __shfl_xor_sync(0xffffffffu, la, 2);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+    float* mw = mo + warp * gr * D;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const int dd = c * 16 + 4 * q4;
+      const float(&ev)[4] = o[2 * c];
+      const float(&od)[4] = o[2 * c + 1];
+      if (r < gr)
+        *reinterpret_cast<float4*>(mw + r * D + dd) = make_float4(ev[0], od[0], ev[1], od[1]);
+      if (r + 8 < gr)
+        *reinterpret_cast<float4*>(mw + (r + 8) * D + dd) = make_float4(ev[2], od[2], ev[3], od[3]);
+    }
+    if (q4 == 0) {
+      mm[warp * 16 + r] = m_a;
+      mm[warp * 16 + r + 8] = m_b;
+      ml[warp * 16 + r] = la;
+      ml[warp * 16 + r + 8] = lb;
+    }
+  }
+};
+
+// Scales of list entry i (block id, plane and KV head resolved by compact_ids); a
+// page outside the pool reads as zeros.
+__device__ __forceinline__ void entry_scales(const AttnArgs& a, int beta, int plane, int g,
+                                             float& ks, float& vs) {
+  const int64_t at =
+      (a.pg.table == nullptr ? (int64_t)plane * a.nblk + beta : (int64_t)plane) * a.h + g;
+  ks = plane < 0 ? 1.f : __ldg(a.ks + at);
+  vs = plane < 0 ? 1.f : __ldg(a.vs + at);
+}
+
 // Merge of NC warp states for tile row `row`, dims [dim, dim + 4) (dim a
 // multiple of 4): normalised output and natural-log LSE (-inf and 0 when no key
 // was seen).  The warps' weights are computed once for the four dims.
@@ -426,7 +730,7 @@ __device__ __forceinline__ void consumer_sync(int nthreads) {
 // Each entry is (block id in the low 16 bits, row offset in the high bits); the
 // row supplies the sequence and the KV head.  Waits are bounded; before leaving,
 // the producer waits for its copies still in flight.
-template <int D>
+template <int D, bool Q8 = false>
 __device__ __forceinline__ void produce(const AttnArgs& a, const CUtensorMap* tmk,
                                         const CUtensorMap* tmv, const int32_t* list,
                                         const int32_t* plist, const int32_t* glist, int n,
@@ -462,11 +766,16 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const CUtensorMap* tm
     const uint32_t full = full0 + 8 * s;
     mbar_arrive_expect_tx(full, a.stage_bytes);
     const uint32_t kdst = sbase + (uint32_t)s * a.stage_bytes;
-    const uint32_t vdst = kdst + NH * half_bytes;
+    if constexpr (Q8) {
+      tma_load_4d(kdst, tmk, full, 0, g, tok, plane);
+      tma_load_4d(kdst + D * a.block, tmv, full, 0, g, tok, plane);
+    } else {
+      const uint32_t vdst = kdst + NH * half_bytes;
 #pragma unroll
-    for (int hh = 0; hh < NH; ++hh) {
-      tma_load_4d(kdst + hh * half_bytes, tmk, full, hh * 64, g, tok, plane);
-      tma_load_4d(vdst + hh * half_bytes, tmv, full, hh * 64, g, tok, plane);
+      for (int hh = 0; hh < NH; ++hh) {
+        tma_load_4d(kdst + hh * half_bytes, tmk, full, hh * 64, g, tok, plane);
+        tma_load_4d(vdst + hh * half_bytes, tmv, full, hh * 64, g, tok, plane);
+      }
     }
     ++issued;
   }
@@ -539,7 +848,7 @@ __device__ __forceinline__ int compact_ids(const AttnArgs& a, int64_t s0, int64_
 }
 
 // ------------------------------------------------------- one CTA per row
-template <int D>
+template <int D, class WS>
 __global__ void __launch_bounds__(5 * 32, 1)
     sparse_attn_rows_kernel(const __grid_constant__ CUtensorMap tmk,
                             const __grid_constant__ CUtensorMap tmv, AttnArgs a) {
@@ -569,7 +878,7 @@ __global__ void __launch_bounds__(5 * 32, 1)
     fence_mbar_init();
   }
   // the consumers load their queries while the list is built
-  WarpState<D> ws;
+  WS ws;
   const RowGeo rg = row_geo(a, rowg);
   if (warp == NC) {
     // after an earlier timeout the kernel does nothing (status read first: its
@@ -585,22 +894,35 @@ __global__ void __launch_bounds__(5 * 32, 1)
   const int n = *n_list;
   if (n < 0) return;
   if (warp == NC) {
-    if (lane == 0 && n > 0) produce<D>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
+    if (lane == 0 && n > 0)
+      produce<D, WS::kQ8>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
     return;
   }
+  const int step = nsub >= NC ? 1 : NC / nsub;  // a warp takes every step-th entry
+  float ks_n = 1.f, vs_n = 1.f;                 // scales of this warp's next entry
+  auto next_scales = [&](int i) {
+    if (WS::kQ8 && i < n) entry_scales(a, list[i] & 0xffff, plist[i], glist[i], ks_n, vs_n);
+  };
+  next_scales(nsub >= NC ? 0 : warp / nsub);
   for (int i = 0; i < n; ++i) {
     const int u0 = i * nsub;
     const int st0 = (warp - (u0 % NC) + NC) % NC;  // first slice of block i owned by this warp
     if (st0 >= nsub) continue;
     const int s = i % a.stages;
+    const float ks = ks_n, vs = vs_n;
+    next_scales(i + step);
     if (!mbar_wait_warp(full0 + 8 * s, (i / a.stages) & 1, a.st, 3u, a.wait_ns)) break;
     const uint32_t kbase = sbase + (uint32_t)s * a.stage_bytes;
-    const uint32_t vbase = kbase + (D / 64) * half_bytes;
+    const uint32_t vbase = kbase + (WS::kQ8 ? D * a.block : (D / 64) * half_bytes);
     const int beta = list[i] & 0xffff;
     bool wrote = false;
     for (int st = st0; st < nsub; st += NC) {
       const int j0 = beta * a.block + st * 16;
-      if (j0 < rg.lim) ws.attend(a, smem, sbase, kbase, vbase, half_bytes, st * 16, j0, rg.lim, lane, wrote);
+      if (j0 >= rg.lim) continue;
+      if constexpr (WS::kQ8)
+        ws.attend(smem, sbase, kbase, vbase, st * 16, j0, rg.lim, lane, ks, vs, wrote);
+      else
+        ws.attend(a, smem, sbase, kbase, vbase, half_bytes, st * 16, j0, rg.lim, lane, wrote);
     }
     if (wrote) fence_proxy_async_smem();
     __syncwarp();
@@ -672,7 +994,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     __syncwarp();
     named_arrive(2, (NC + 1) * 32);
     if (lane == 0 && !skip && n > 0)
-      produce<D>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
+      produce<D, WS::kQ8>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
     return;
   }
   // the consumers load their first row's queries while the list is built
@@ -850,6 +1172,12 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     consumer_sync(NC * 32);  // the merge buffer is free again
   };
 
+  const int step = nsub >= NC ? 1 : NC / nsub;  // a warp takes every step-th entry
+  float ks_n = 1.f, vs_n = 1.f;                 // scales of this warp's next entry
+  auto next_scales = [&](int i) {
+    if (WS::kQ8 && i < n) entry_scales(a, list[i] & 0xffff, plist[i], glist[i], ks_n, vs_n);
+  };
+  next_scales(nsub >= NC ? 0 : warp / nsub);
   for (int i = 0; i < n; ++i) {
     const int e = list[i];
     const int64_t row = r0 + (e >> 16);
@@ -864,6 +1192,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     const int st0 = (warp - (u0 % NC) + NC) % NC;
     if (st0 >= nsub || failed) continue;
     const int s = i % a.stages;
+    const float ks = ks_n, vs = vs_n;
+    next_scales(i + step);
     // After a wait runs out this warp stops computing but keeps walking the list,
     // so that every consumer warp still reaches the same row-boundary barriers.
     if (!mbar_wait_warp(full0 + 8 * s, (i / a.stages) & 1, a.st, 3u, a.wait_ns)) {
@@ -871,12 +1201,16 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
       continue;
     }
     const uint32_t kbase = sbase + (uint32_t)s * a.stage_bytes;
-    const uint32_t vbase = kbase + (D / 64) * half_bytes;
+    const uint32_t vbase = kbase + (WS::kQ8 ? D * a.block : (D / 64) * half_bytes);
     const int beta = e & 0xffff;
     bool wrote = false;
     for (int st = st0; st < nsub; st += NC) {
       const int j0 = beta * a.block + st * 16;
-      if (j0 < rg.lim) ws.attend(a, smem, sbase, kbase, vbase, half_bytes, st * 16, j0, rg.lim, lane, wrote);
+      if (j0 >= rg.lim) continue;
+      if constexpr (WS::kQ8)
+        ws.attend(smem, sbase, kbase, vbase, st * 16, j0, rg.lim, lane, ks, vs, wrote);
+      else
+        ws.attend(a, smem, sbase, kbase, vbase, half_bytes, st * 16, j0, rg.lim, lane, wrote);
     }
     if (wrote) fence_proxy_async_smem();
     __syncwarp();
@@ -895,10 +1229,26 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 // K or V as a 4-D tensor [batch][token][kv head][dim], or for a paged cache
 // [page][token in page][kv head][dim]; one box is 64 dims x 1 head x `block`
 // tokens (128 bytes per row, 128-byte swizzle).
-bool make_kv_map(CUtensorMap* map, const uint16_t* base, const Shape& s, const int64_t* str) {
+bool make_kv_map(CUtensorMap* map, const void* base, const Shape& s, const int64_t* str) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const bool paged = s.pages.table != nullptr;
+  if (s.kv8) {
+    // e4m3 codes: one box is a whole row of d bytes x 1 head x `block` tokens.  L2
+    // fills are kept to the row's 128 bytes: with the heads of a token side by side,
+    // a wider fill would bring rows that no selected block needs.
+    cuuint64_t dims8[4] = {(cuuint64_t)s.d, (cuuint64_t)s.h,
+                           (cuuint64_t)(paged ? s.block : s.max_kv),
+                           (cuuint64_t)(paged ? s.pages.pages : s.batch)};
+    cuuint64_t strides8[3] = {(cuuint64_t)str[2], (cuuint64_t)str[1], (cuuint64_t)str[0]};
+    cuuint32_t box8[4] = {(cuuint32_t)s.d, 1, (cuuint32_t)s.block, 1};
+    cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims8, strides8,
+               box8, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               s.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+  }
   cuuint64_t dims[4] = {(cuuint64_t)s.d, (cuuint64_t)s.h,
                         (cuuint64_t)(paged ? s.block : s.max_kv),
                         (cuuint64_t)(paged ? s.pages.pages : s.batch)};
@@ -906,7 +1256,7 @@ bool make_kv_map(CUtensorMap* map, const uint16_t* base, const Shape& s, const i
                            (cuuint64_t)str[0] * 2};
   cuuint32_t box[4] = {64, 1, (cuuint32_t)s.block, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims,
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
@@ -943,15 +1293,17 @@ struct AttnPlan {
 // Stage count that keeps every block of a stage on the same warps (a warp waits
 // only on the stages of blocks it processes): with fewer 16-token slices per
 // block than consumer warps, a multiple of the warp cycle.
-int stage_count(int want, int nsub, int nc) {
+int stage_count(int want, int nsub, int nc, int most) {
   const int cycle = nsub >= nc ? 1 : nc / nsub;
-  want = max(2, min(8, want));
+  want = max(2, min(most, want));
   return max(cycle, want - want % cycle);
 }
 
 AttnPlan plan_attn(const Shape& s) {
   AttnPlan pl;
-  pl.stage_bytes = 4u * s.d * s.block;  // K and V tiles of one block, bf16
+  const bool kv8 = s.kv8;
+  pl.stage_bytes = (kv8 ? 2u : 4u) * s.d * s.block;  // K and V tiles of one block
+  const int most = kv8 ? 32 : 8;                     // stages
   const int nsub = s.block / 16;
   const int64_t rows_g = (int64_t)s.batch * s.n_q * s.h;
   pl.total = rows_g * s.topk;
@@ -976,14 +1328,14 @@ AttnPlan plan_attn(const Shape& s) {
     const size_t fixed = 1024 + merge_r + 4 * (3 * (size_t)pl.list_cap + 1);
     const size_t cap = (size_t)max_smem_optin();
     const int fit = cap > fixed ? (int)((cap - fixed) / (pl.stage_bytes + 16)) : 0;
-    pl.stages = stage_count(fit, nsub, kStreamNC);  // fit >= 3 for every supported shape
+    pl.stages = stage_count(fit, nsub, kStreamNC, most);  // fit >= 3 for every supported shape
     pl.region_bytes = pl.stages * pl.stage_bytes + merge_r;
     pl.merge_off = pl.stages * pl.stage_bytes;
   } else {
     // Two CTAs per SM when the stages allow it, else one with deeper buffering.
     int want = (int)((100u * 1024u) / pl.stage_bytes);
     if (want < 2) want = min(4, (int)((200u * 1024u) / pl.stage_bytes));
-    pl.stages = stage_count(want, nsub, 4);
+    pl.stages = stage_count(want, nsub, 4, 8);
     pl.region_bytes = max(pl.stages * pl.stage_bytes, merge_bytes);
     pl.merge_off = 0;
     pl.ctas = (int)rows_g;
@@ -1011,7 +1363,7 @@ bool make_rows_map(CUtensorMap* map, uint16_t* base, int64_t rows, int d) {
 
 size_t attn_partial_bytes(const Shape& s) {
   const AttnPlan pl = plan_attn(s);
-  if (!pl.stream) return kv_attn_supported(s) ? kv_workspace_bytes(s) : 0;
+  if (!pl.stream) return !s.kv8 && kv_attn_supported(s) ? kv_workspace_bytes(s) : 0;
   const size_t n = (size_t)s.batch * s.n_q * s.H * pl.smax;
   const size_t rows_g = (size_t)s.batch * s.n_q * s.h;
   return n * (size_t)(s.d + 1) * sizeof(float) + rows_g * sizeof(int) + 512;
@@ -1019,7 +1371,7 @@ size_t attn_partial_bytes(const Shape& s) {
 
 int attn_launches(const Shape& s) {
   const AttnPlan pl = plan_attn(s);
-  return !pl.stream && kv_attn_supported(s) ? kv_launches(s) : 1;
+  return !pl.stream && !s.kv8 && kv_attn_supported(s) ? kv_launches(s) : 1;
 }
 
 int* attn_merge_counters(const Shape& s, void* partials, int* count) {
@@ -1033,8 +1385,8 @@ int* attn_merge_counters(const Shape& s, void* partials, int* count) {
       (reinterpret_cast<uintptr_t>(part_lse + nrow_h * pl.smax) + 255) & ~uintptr_t(255));
 }
 
-cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const uint16_t* k,
-                               const uint16_t* v, const int32_t* ids, uint16_t* out, float* lse,
+cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const void* k,
+                               const void* v, const int32_t* ids, uint16_t* out, float* lse,
                                void* partials, size_t partial_bytes, DeviceStatus* st,
                                cudaStream_t stream, bool counters_zeroed, int* fixed_counters) {
   const AttnPlan pl = plan_attn(s);
@@ -1078,28 +1430,33 @@ cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const uint16_t
   a.st = st;
   a.wait_ns = 4000000000ull;  // 4 s: far above any healthy wait, even under a profiler
   a.pg = s.pages;
+  a.ks = s.ks;
+  a.vs = s.vs;
   cudaError_t err;
-  if (!pl.stream && kv_attn_supported(s)) {
+  if (!pl.stream && !s.kv8 && kv_attn_supported(s)) {
     CUtensorMap tmq;
     if (!make_q_group_map(&tmq, q, s)) return cudaErrorInvalidValue;
     return launch_kv_attn(s, tmq, tmk, tmv, q, ids, out, lse, partials, partial_bytes, st, stream);
   }
+  const bool kv8 = s.kv8;
+  auto launch = [&](auto kernel, int threads) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)pl.smem_bytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)pl.ctas), dim3(threads), pl.smem_bytes, stream, tmk,
+                      tmv, a);
+  };
   if (!pl.stream) {
-    const dim3 grid((unsigned)pl.ctas);
-    if (s.d == 128) {
-      err = cudaFuncSetAttribute(sparse_attn_rows_kernel<128>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem_bytes);
-      if (err != cudaSuccess) return err;
-      err = launch_pdl(sparse_attn_rows_kernel<128>, grid, dim3(5 * 32), pl.smem_bytes, stream, tmk,
-                       tmv, a);
-    } else {
-      err = cudaFuncSetAttribute(sparse_attn_rows_kernel<64>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem_bytes);
-      if (err != cudaSuccess) return err;
-      err = launch_pdl(sparse_attn_rows_kernel<64>, grid, dim3(5 * 32), pl.smem_bytes, stream, tmk,
-                       tmv, a);
+    constexpr int NT = 5 * 32;
+    if (kv8) {
+      if (s.d == 128)
+        return s.G <= 8 ? launch(sparse_attn_rows_kernel<128, WarpStateTQ<128>>, NT)
+                        : launch(sparse_attn_rows_kernel<128, WarpStateQ<128>>, NT);
+      return s.G <= 8 ? launch(sparse_attn_rows_kernel<64, WarpStateTQ<64>>, NT)
+                      : launch(sparse_attn_rows_kernel<64, WarpStateQ<64>>, NT);
     }
-    return err;
+    return s.d == 128 ? launch(sparse_attn_rows_kernel<128, WarpState<128>>, NT)
+                      : launch(sparse_attn_rows_kernel<64, WarpState<64>>, NT);
   }
   const size_t nrow_h = (size_t)s.batch * s.n_q * s.H;
   if (partials == nullptr || partial_bytes < attn_partial_bytes(s)) return cudaErrorInvalidValue;
@@ -1113,20 +1470,20 @@ cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const uint16_t
     err = cudaMemsetAsync(a.counters, 0, (size_t)ncounters * sizeof(int), stream);
     if (err != cudaSuccess) return err;
   }
-  const dim3 grid((unsigned)pl.ctas);
   constexpr int NT = (kStreamNC + 1) * 32;
-  auto run = [&](auto kernel) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)pl.smem_bytes);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, grid, dim3(NT), pl.smem_bytes, stream, tmk, tmv, a);
-  };
   // groups of up to 8 heads take the swapped MMA operands
+  if (kv8) {
+    if (s.d == 128)
+      return s.G <= 8 ? launch(sparse_attn_stream_kernel<128, kStreamNC, WarpStateTQ<128>>, NT)
+                      : launch(sparse_attn_stream_kernel<128, kStreamNC, WarpStateQ<128>>, NT);
+    return s.G <= 8 ? launch(sparse_attn_stream_kernel<64, kStreamNC, WarpStateTQ<64>>, NT)
+                    : launch(sparse_attn_stream_kernel<64, kStreamNC, WarpStateQ<64>>, NT);
+  }
   if (s.d == 128)
-    return s.G <= 8 ? run(sparse_attn_stream_kernel<128, kStreamNC, WarpStateT<128>>)
-                    : run(sparse_attn_stream_kernel<128, kStreamNC, WarpState<128>>);
-  return s.G <= 8 ? run(sparse_attn_stream_kernel<64, kStreamNC, WarpStateT<64>>)
-                  : run(sparse_attn_stream_kernel<64, kStreamNC, WarpState<64>>);
+    return s.G <= 8 ? launch(sparse_attn_stream_kernel<128, kStreamNC, WarpStateT<128>>, NT)
+                    : launch(sparse_attn_stream_kernel<128, kStreamNC, WarpState<128>>, NT);
+  return s.G <= 8 ? launch(sparse_attn_stream_kernel<64, kStreamNC, WarpStateT<64>>, NT)
+                  : launch(sparse_attn_stream_kernel<64, kStreamNC, WarpState<64>>, NT);
 }
 
 }  // namespace msa

@@ -13,8 +13,11 @@ present, these functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -39,12 +42,20 @@ MSA_OP_INDEX_CANDIDATES = 5
 MSA_OP_SELECT_CANDIDATES = 6
 MSA_OP_SHARD_LENGTHS = 7
 MSA_OP_INDEX_TOPK = 8
+MSA_OP_APPEND_KV_Q8 = 9
+MSA_OP_READ_KV_Q8 = 10
+MSA_OP_BLOCK_SCORES_Q8 = 11
+MSA_OP_INDEX_SELECT_Q8 = 12
+MSA_OP_SPARSE_ATTN_Q8 = 13
+MSA_OP_FORWARD_Q8 = 14
 
 EXPORTED = ("msa_workspace_size", "msa_index_select", "msa_sparse_attn", "msa_forward",
             "msa_get_device_status", "msa_workspace_init", "msa_selftest_wait_timeout",
             "msa_launch_count", "msa_sparse_attn_noalloc", "msa_status_string", "msa_append_kv",
             "msa_block_scores", "msa_index_candidates", "msa_select_candidates",
-            "msa_merge_partials", "msa_shard_lengths", "msa_index_topk")
+            "msa_merge_partials", "msa_shard_lengths", "msa_index_topk", "msa_append_kv_q8",
+            "msa_read_kv_q8", "msa_block_scores_q8", "msa_index_select_q8", "msa_sparse_attn_q8",
+            "msa_forward_q8")
 
 
 class MsaError(RuntimeError):
@@ -118,6 +129,18 @@ def load_library():
             lib.msa_merge_partials.restype = I
             lib.msa_shard_lengths.argtypes = [P, ctypes.c_int64, ctypes.c_int64, P, P, S, P]
             lib.msa_shard_lengths.restype = I
+            lib.msa_append_kv_q8.argtypes = [P] * 10 + [P, S, P]
+            lib.msa_append_kv_q8.restype = I
+            lib.msa_read_kv_q8.argtypes = [P] * 7 + [ctypes.c_int64] + [P] * 3 + [P, S, P]
+            lib.msa_read_kv_q8.restype = I
+            lib.msa_block_scores_q8.argtypes = [P] * 5 + [P, S, P]
+            lib.msa_block_scores_q8.restype = I
+            lib.msa_index_select_q8.argtypes = [P] * 6 + [P, S, P]
+            lib.msa_index_select_q8.restype = I
+            lib.msa_sparse_attn_q8.argtypes = [P] * 9 + [P, S, P]
+            lib.msa_sparse_attn_q8.restype = I
+            lib.msa_forward_q8.argtypes = [P] * 13 + [P, S, P]
+            lib.msa_forward_q8.restype = I
             lib.msa_launch_count.argtypes = [P, I]
             lib.msa_launch_count.restype = I
             lib.msa_status_string.argtypes = [I]
@@ -177,11 +200,19 @@ def make_params(*, batch, n_q, max_kv, H, h, d, d_idx, block, topk, causal=True,
 
 
 class Workspace:
-    """A device buffer for the library's workspace, grown on demand."""
+    """A device buffer for the library's workspace, grown on demand.  Calls that share
+    one must be ordered on one stream."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
         self.buf = None
+        self._held: list = []  # buffers that captured graphs write to
+
+    def hold(self):
+        """Keeps the present buffer alive past a later growth: a graph captured with it
+        holds its address."""
+        if not self._held or self._held[-1] is not self.buf:
+            self._held.append(self.buf)
 
     def get(self, nbytes: int) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
@@ -516,3 +547,346 @@ def msa_index_topk(q_idx, k_idx, *, block, topk, causal=True, force_own_block=Fa
                                          ws.numel(), _stream(stream)), "msa_index_topk")
     return (block_ids, block_scores) if return_scores else block_ids
 
+
+
+# ------------------------------------------------------------------ 8-bit cache
+class Q8Cache(NamedTuple):
+    """The tensors of an 8-bit KV cache, in the order in which the calls take them: e4m3
+    codes [batch, max_kv, h, d] (k_idx: [batch, max_kv, d_idx]) with fp32 scales [batch,
+    nblk, h] ([batch, nblk]), or page pools [num_pages, block, h, d] with [num_pages, h]."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_idx: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    k_idx_scale: torch.Tensor
+
+
+def q8_cache(*, h, d, d_idx, block, batch=None, max_kv=None, num_pages=None, device="cuda"):
+    """An empty 8-bit cache: contiguous (``batch``, ``max_kv``), or a page pool
+    (``num_pages``).  A head's rows lie next to each other in memory, so that a block of
+    one head is one contiguous piece."""
+    if (num_pages is None) == (batch is None or max_kv is None):
+        raise ValueError("give either batch and max_kv, or num_pages")
+    planes, rows = (batch, max_kv) if num_pages is None else (num_pages, block)
+    scales = (planes, -(-rows // block)) if num_pages is None else (planes,)
+
+    def codes(*shape):
+        return torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+
+    def ones(*shape):
+        return torch.ones(shape, dtype=torch.float32, device=device)
+
+    return Q8Cache(codes(planes, h, rows, d).transpose(1, 2), codes(planes, h, rows, d).transpose(1, 2),
+                   codes(planes, rows, d_idx), ones(*scales, h), ones(*scales, h), ones(*scales))
+
+
+# msa_params_t as one packed record: a decode step makes several calls of a few
+# microseconds each, and filling the ctypes structure field by field takes longer
+# than some of the kernels.
+_PARAMS = struct.Struct("11ifP17qP2q")
+assert _PARAMS.size == ctypes.sizeof(Params)
+_NO3 = (0, 0, 0)
+_F8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _q8_codes(name, t, planes, rows, tail, dev):
+    """Checks a code tensor and returns its outer strides."""
+    if t.dtype not in _F8:
+        raise ValueError("%s must hold e4m3 codes (float8_e4m3fn or uint8)" % name)
+    if t.device != dev or t.shape[0] != planes or t.shape[1] != rows or t.shape[2:] != tail:
+        raise ValueError("%s has shape %s on %s" % (name, tuple(t.shape), t.device))
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError("innermost axis of %s must be contiguous" % name)
+    return st[:-1]
+
+
+def _q8_scale(name, t, shape, dev):
+    if t.dtype != torch.float32 or t.device != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a dense fp32 tensor of shape %s on %s" % (name, shape, dev))
+
+
+def _q8_dense(name, t, shape, dtype, dev):
+    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a dense %s tensor of shape %s on %s"
+                         % (name, dtype, tuple(shape), dev))
+
+
+class _Q8Call:
+    """One call's cache geometry, stream and workspace."""
+
+    def __init__(self, dev, batch, codes, block, seq_lens, block_table, max_kv, stream):
+        if dev.type != "cuda":
+            raise ValueError("the 8-bit cache calls need CUDA tensors")
+        self.dev = dev
+        self.block = block
+        self.planes = codes.shape[0]
+        self.paged = block_table is not None
+        if self.paged:
+            if max_kv is None:
+                raise ValueError("a paged KV cache needs max_kv")
+            self.max_kv, self.rows, self.pages = int(max_kv), block, self.planes
+            if (block_table.dtype != torch.int32 or block_table.dim() != 2
+                    or block_table.device != dev or block_table.shape[0] != batch
+                    or block_table.stride(1) != 1 or block_table.shape[1] * block < self.max_kv):
+                raise ValueError("block_table must be int32 [batch, >= ceil(max_kv / block)]")
+            self.table = (block_table.data_ptr(), block_table.stride(0) if batch > 1
+                          else max(block_table.stride(0), block_table.shape[1]))
+        else:
+            if self.planes != batch:
+                raise ValueError("the cache holds %d sequences, not %d" % (self.planes, batch))
+            self.max_kv = self.rows = codes.shape[1]
+            if max_kv is not None and int(max_kv) != self.max_kv:
+                raise ValueError("max_kv is the cache's token axis, %d" % self.max_kv)
+            self.pages, self.table = 0, (0, 0)
+        self.nblk = -(-self.max_kv // block)
+        self.scales = (self.planes,) if self.paged else (batch, self.nblk)
+        self.lens = 0
+        if seq_lens is not None:
+            _q8_dense("seq_lens", seq_lens, (batch,), torch.int32, dev)
+            self.lens = seq_lens.data_ptr()
+        self.stream = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+                       else stream.cuda_stream)
+
+    def params(self, batch, n_q, H, h, d, d_idx, topk, causal=True, force=False, scale=0.0,
+               q=_NO3, k=_NO3, v=_NO3, qi=_NO3, ki=(0, 0), o=_NO3):
+        return _PARAMS.pack(batch, n_q, self.max_kv, H, h, d, d_idx, self.block, topk,
+                            bool(causal), bool(force), scale, self.lens, *q, *k, *v, *qi, *ki, *o,
+                            self.table[0], self.table[1], self.pages)
+
+    def run(self, what, op, params, workspace, *args):
+        lib = load_library()
+        need = lib.msa_workspace_size(params, op)
+        if need == 0:  # bad parameters: the call itself says which
+            need = STATUS_BYTES
+        if workspace is None:
+            workspace = self.default_workspace()
+        buf = workspace.buf
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+        if buf is None or buf.numel() < need:
+            if capturing:
+                raise RuntimeError("the workspace cannot grow while a graph is captured: run the "
+                                   "call once before, or pass a Workspace that is large enough")
+            with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, self.dev)):
+                buf = workspace.get(need)
+        if capturing:
+            workspace.hold()
+        rc = getattr(lib, what)(params, *args, buf.data_ptr(), buf.numel(), self.stream)
+        if rc != MSA_OK:
+            raise MsaError(rc, what)
+
+    def default_workspace(self):
+        """The device's workspace, one for each stream other than the default one."""
+        key = self.dev.index if self.stream == 0 else (self.dev.index, self.stream)
+        if key not in _default_ws:
+            _default_ws[key] = Workspace(self.dev)
+        return _default_ws[key]
+
+
+def _on_device(f):
+    """Runs a call with its tensors' device current."""
+
+    @functools.wraps(f)
+    def call(first, *args, **kw):
+        dev = first.device
+        if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+            return f(first, *args, **kw)
+        with torch.cuda.device(dev):
+            return f(first, *args, **kw)
+
+    return call
+
+
+def _need(x, what):
+    if x is None:
+        raise ValueError("%s is missing" % what)
+    return x
+
+
+def _bf16_outer(name, t, dev):
+    """Strides of a bf16 tensor's outer axes."""
+    if t.dtype != torch.bfloat16 or t.device != dev or t.stride(-1) != 1:
+        raise ValueError("%s must be bf16 on %s, its innermost axis contiguous" % (name, dev))
+    return t.stride()[:-1]
+
+
+@_on_device
+def msa_append_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new=None, v_new=None,
+                     k_idx_new=None, *, block, seq_lens=None, block_table=None, max_kv=None,
+                     workspace: Workspace | None = None, stream=None):
+    """msa_append_kv into an 8-bit cache: the bf16 rows k_new / v_new [b, n_new, h, d] and
+    k_idx_new [b, n_new, d_idx] (dense) are quantised into positions L_b - n_new + t, and
+    the scales of the blocks they fall into are set (see ``include/msa.h``).  Any of the
+    new tensors may be None (its part of the cache is not written)."""
+    ref = next((t for t in (k_new, v_new, k_idx_new) if t is not None), None)
+    if ref is None:
+        raise ValueError("no new rows")
+    b, n, h, d = ref.shape[0], ref.shape[1], k.shape[2], k.shape[3]
+    d_idx = k_idx.shape[-1]
+    c = _Q8Call(k.device, b, k, block, seq_lens, block_table, max_kv, stream)
+    ks, vs, kis = _q8_strides(c, k, v, k_idx, k_scale, v_scale, k_idx_scale, h, d, d_idx)
+    for name, t, tail in (("k_new", k_new, (h, d)), ("v_new", v_new, (h, d)),
+                          ("k_idx_new", k_idx_new, (d_idx,))):
+        if t is not None:
+            _q8_dense(name, t, (b, n) + tail, torch.bfloat16, c.dev)
+    p = c.params(b, n, h, h, d, d_idx, 1, k=ks, v=vs, ki=kis)
+    c.run("msa_append_kv_q8", MSA_OP_APPEND_KV_Q8, p, workspace, _ptr(k_new), _ptr(v_new),
+          _ptr(k_idx_new), k.data_ptr(), v.data_ptr(), k_idx.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), k_idx_scale.data_ptr())
+
+
+def _q8_strides(c, k, v, k_idx, k_scale, v_scale, k_idx_scale, h, d, d_idx):
+    ks = _q8_codes("k", k, c.planes, c.rows, (h, d), c.dev)
+    vs = _q8_codes("v", v, c.planes, c.rows, (h, d), c.dev)
+    kis = _q8_codes("k_idx", k_idx, c.planes, c.rows, (d_idx,), c.dev)
+    _q8_scale("k_scale", k_scale, c.scales + (h,), c.dev)
+    _q8_scale("v_scale", v_scale, c.scales + (h,), c.dev)
+    _q8_scale("k_idx_scale", k_idx_scale, c.scales, c.dev)
+    return ks, vs, kis
+
+
+@_on_device
+def msa_read_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, *, n, token_base=0, block,
+                   seq_lens=None, block_table=None, max_kv=None, k_out=None, v_out=None,
+                   k_idx_out=None, workspace: Workspace | None = None, stream=None):
+    """Rows [token_base, token_base + n) of every sequence of an 8-bit cache as bf16:
+    (k [b, n, h, d], v, k_idx [b, n, d_idx]).  Rows at positions past a sequence's end are
+    left as they were in the given outputs, and are zeros in those made here."""
+    h, d, d_idx = k.shape[2], k.shape[3], k_idx.shape[-1]
+    b = block_table.shape[0] if block_table is not None else k.shape[0]
+    c = _Q8Call(k.device, b, k, block, seq_lens, block_table, max_kv, stream)
+    ks, vs, kis = _q8_strides(c, k, v, k_idx, k_scale, v_scale, k_idx_scale, h, d, d_idx)
+    outs = []
+    for name, t, tail in (("k_out", k_out, (h, d)), ("v_out", v_out, (h, d)),
+                          ("k_idx_out", k_idx_out, (d_idx,))):
+        if t is None:
+            t = torch.zeros((b, n) + tail, dtype=torch.bfloat16, device=c.dev)
+        else:
+            _q8_dense(name, t, (b, n) + tail, torch.bfloat16, c.dev)
+        outs.append(t)
+    p = c.params(b, n, h, h, d, d_idx, 1, k=ks, v=vs, ki=kis)
+    c.run("msa_read_kv_q8", MSA_OP_READ_KV_Q8, p, workspace, k.data_ptr(), v.data_ptr(),
+          k_idx.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_idx_scale.data_ptr(),
+          int(token_base), *(t.data_ptr() for t in outs))
+    return tuple(outs)
+
+
+def _q8_index(q_idx, k_idx, k_idx_scale, block, topk, causal, force_own_block, seq_lens,
+              block_table, max_kv, stream):
+    b, n_q, h, d_idx = q_idx.shape
+    c = _Q8Call(q_idx.device, b, k_idx, block, seq_lens, block_table, max_kv, stream)
+    kis = _q8_codes("k_idx", k_idx, c.planes, c.rows, (d_idx,), c.dev)
+    _q8_scale("k_idx_scale", k_idx_scale, c.scales, c.dev)
+    p = c.params(b, n_q, h, h, 64, d_idx, topk, causal, force_own_block,
+                 qi=_bf16_outer("q_idx", q_idx, c.dev), ki=kis)
+    return c, p
+
+
+def _q8_out(t, name, shape, dtype, dev, wanted=True):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev) if wanted else None
+    _q8_dense(name, t, shape, dtype, dev)
+    return t
+
+
+@_on_device
+def msa_block_scores_q8(q_idx, k_idx, k_idx_scale, *, block, causal=True, seq_lens=None,
+                        block_scores=None, block_table=None, max_kv=None,
+                        workspace: Workspace | None = None, stream=None):
+    """msa_block_scores over the 8-bit index key: fp32 [b, n_q, h, nblk]."""
+    c, p = _q8_index(q_idx, k_idx, k_idx_scale, block, 1, causal, False, seq_lens, block_table,
+                     max_kv, stream)
+    block_scores = _q8_out(block_scores, "block_scores", q_idx.shape[:3] + (c.nblk,),
+                           torch.float32, c.dev)
+    c.run("msa_block_scores_q8", MSA_OP_BLOCK_SCORES_Q8, p, workspace, q_idx.data_ptr(),
+          k_idx.data_ptr(), k_idx_scale.data_ptr(), block_scores.data_ptr())
+    return block_scores
+
+
+@_on_device
+def msa_index_select_q8(q_idx, k_idx, k_idx_scale, *, block, topk, causal=True,
+                        force_own_block=False, seq_lens=None, return_scores=False,
+                        block_ids=None, block_scores=None, block_table=None, max_kv=None,
+                        workspace: Workspace | None = None, stream=None):
+    """msa_index_select over the 8-bit index key: block ids int32 [b, n_q, h, topk] (and the
+    fp32 block scores if asked)."""
+    c, p = _q8_index(q_idx, k_idx, k_idx_scale, block, topk, causal, force_own_block, seq_lens,
+                     block_table, max_kv, stream)
+    lead = q_idx.shape[:3]
+    block_ids = _q8_out(block_ids, "block_ids", lead + (topk,), torch.int32, c.dev)
+    block_scores = _q8_out(block_scores, "block_scores", lead + (c.nblk,), torch.float32, c.dev,
+                           return_scores)
+    c.run("msa_index_select_q8", MSA_OP_INDEX_SELECT_Q8, p, workspace, q_idx.data_ptr(),
+          k_idx.data_ptr(), k_idx_scale.data_ptr(), block_ids.data_ptr(), _ptr(block_scores))
+    return (block_ids, block_scores) if return_scores else block_ids
+
+
+@_on_device
+def msa_sparse_attn_q8(q, k, v, k_scale, v_scale, block_ids, *, block, causal=True,
+                       seq_lens=None, softmax_scale=0.0, return_lse=False, out=None, lse=None,
+                       block_table=None, max_kv=None, workspace: Workspace | None = None,
+                       stream=None):
+    """msa_sparse_attn over the 8-bit cache: bf16 output [b, n_q, H, d] (and fp32 lse
+    [b, n_q, H] if asked)."""
+    b, n_q, H, d = q.shape
+    h = k.shape[2]
+    c = _Q8Call(q.device, b, k, block, seq_lens, block_table, max_kv, stream)
+    ks = _q8_codes("k", k, c.planes, c.rows, (h, d), c.dev)
+    vs = _q8_codes("v", v, c.planes, c.rows, (h, d), c.dev)
+    _q8_scale("k_scale", k_scale, c.scales + (h,), c.dev)
+    _q8_scale("v_scale", v_scale, c.scales + (h,), c.dev)
+    topk = block_ids.shape[-1]
+    _q8_dense("block_ids", block_ids, (b, n_q, h, topk), torch.int32, c.dev)
+    if out is None:
+        out = torch.empty((b, n_q, H, d), dtype=torch.bfloat16, device=c.dev)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the queries' shape")
+    lse = _q8_out(lse, "lse", (b, n_q, H), torch.float32, c.dev, return_lse)
+    p = c.params(b, n_q, H, h, d, 32, topk, causal, scale=softmax_scale,
+                 q=_bf16_outer("q", q, c.dev), k=ks, v=vs, o=_bf16_outer("out", out, c.dev))
+    c.run("msa_sparse_attn_q8", MSA_OP_SPARSE_ATTN_Q8, p, workspace, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_ids.data_ptr(),
+          out.data_ptr(), _ptr(lse))
+    return (out, lse) if return_lse else out
+
+
+@_on_device
+def msa_forward_q8(q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, *, block, topk,
+                   causal=True, force_own_block=False, seq_lens=None, softmax_scale=0.0,
+                   out=None, block_ids=None, block_scores=None, lse=None, return_ids=False,
+                   return_scores=False, return_lse=False, block_table=None, max_kv=None,
+                   workspace: Workspace | None = None, stream=None):
+    """msa_forward over the 8-bit cache; returns out, plus (ids, scores, lse) when asked,
+    in that order."""
+    b, n_q, H, d = q.shape
+    h, d_idx = k.shape[2], q_idx.shape[-1]
+    c = _Q8Call(q.device, b, k, block, seq_lens, block_table, max_kv, stream)
+    ks, vs, kis = _q8_strides(c, k, v, k_idx, k_scale, v_scale, k_idx_scale, h, d, d_idx)
+    if q_idx.shape != (b, n_q, h, d_idx):
+        raise ValueError("q_idx must have shape [b, n_q, h, d_idx]")
+    if out is None:
+        out = torch.empty((b, n_q, H, d), dtype=torch.bfloat16, device=c.dev)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the queries' shape")
+    lead = (b, n_q, h)
+    block_ids = _q8_out(block_ids, "block_ids", lead + (topk,), torch.int32, c.dev, return_ids)
+    block_scores = _q8_out(block_scores, "block_scores", lead + (c.nblk,), torch.float32, c.dev,
+                           return_scores)
+    lse = _q8_out(lse, "lse", (b, n_q, H), torch.float32, c.dev, return_lse)
+    p = c.params(b, n_q, H, h, d, d_idx, topk, causal, force_own_block, softmax_scale,
+                 q=_bf16_outer("q", q, c.dev), k=ks, v=vs, qi=_bf16_outer("q_idx", q_idx, c.dev),
+                 ki=kis, o=_bf16_outer("out", out, c.dev))
+    c.run("msa_forward_q8", MSA_OP_FORWARD_Q8, p, workspace, q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), q_idx.data_ptr(), k_idx.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), k_idx_scale.data_ptr(), out.data_ptr(), _ptr(block_ids),
+          _ptr(block_scores), _ptr(lse))
+    res = [out]
+    if return_ids:
+        res.append(block_ids)
+    if return_scores:
+        res.append(block_scores)
+    if return_lse:
+        res.append(lse)
+    return res[0] if len(res) == 1 else tuple(res)

@@ -79,6 +79,7 @@ extern "C" {
 #endif
 
 typedef uint16_t msa_bf16_t;          /* raw bf16 bits */
+typedef uint8_t msa_e4m3_t;           /* raw e4m3 bits (4 exponent, 3 mantissa bits, no infinity) */
 typedef struct CUstream_st* msa_stream_t; /* same handle as cudaStream_t; NULL = legacy default */
 
 typedef enum msa_status {
@@ -100,7 +101,13 @@ typedef enum msa_op {
   MSA_OP_INDEX_CANDIDATES = 5,
   MSA_OP_SELECT_CANDIDATES = 6,
   MSA_OP_SHARD_LENGTHS = 7,
-  MSA_OP_INDEX_TOPK = 8
+  MSA_OP_INDEX_TOPK = 8,
+  MSA_OP_APPEND_KV_Q8 = 9,
+  MSA_OP_READ_KV_Q8 = 10,
+  MSA_OP_BLOCK_SCORES_Q8 = 11,
+  MSA_OP_INDEX_SELECT_Q8 = 12,
+  MSA_OP_SPARSE_ATTN_Q8 = 13,
+  MSA_OP_FORWARD_Q8 = 14
 } msa_op_t;
 
 typedef struct msa_params {
@@ -329,6 +336,97 @@ MSA_API msa_status_t msa_sparse_attn_noalloc(const msa_params_t* params, const m
                                              const msa_bf16_t* k, const msa_bf16_t* v,
                                              const int32_t* block_ids, msa_bf16_t* out,
                                              float* lse, msa_stream_t stream);
+
+/* ------------------------------------------------------------- 8-bit KV cache
+ * K, V and K_idx held as e4m3 codes with one fp32 scale for each (block of tokens,
+ * KV head) of K and of V and one for each block of K_idx; a value is code * scale.
+ * Half the bytes of the bf16 cache, and a decode step reads half as much.
+ *
+ *   k, v   e4m3 [batch, max_kv, h, d]   k_scale, v_scale  fp32 [batch, nblk, h]
+ *   k_idx  e4m3 [batch, max_kv, d_idx]  k_idx_scale       fp32 [batch, nblk]
+ * or, with block_table, pools of pages
+ *   k, v   e4m3 [num_pages, block, h, d]  k_scale, v_scale  fp32 [num_pages, h]
+ *   k_idx  e4m3 [num_pages, block, d_idx] k_idx_scale       fp32 [num_pages]
+ * k/v_strides and ki_strides count codes (bytes) and are multiples of 16; any order
+ * of the outer axes will do (with a head's rows next to each other, a block of one
+ * head is one contiguous piece).  Scales are dense.  The rest of msa_params_t means
+ * what it means above, and queries, new rows and outputs stay bf16.
+ *
+ * Scales.  msa_append_kv_q8 makes powers of two from 2^-100 to 2^120, and where a
+ * block already holds rows it requires one there.  The readers take any positive
+ * finite scale; for one that is not a power of two, code * scale is rounded to bf16
+ * by msa_read_kv_q8 and, with n_q > 1, in the index key of the score calls. */
+
+/* Decode-step or prompt write into the 8-bit cache: the rows of msa_append_kv,
+ * quantised.  For every (block, head) that receives rows, with x those rows:
+ *   need = the smallest power of two >= 2^-100 with max |x| <= 448 * need
+ *   s'   = need, or max(s, need) when the block holds older rows (rows of this
+ *          sequence before position L_b - n_q in the same block)
+ *   new rows:   code = e4m3(x / s')        older rows: code' = e4m3(code * s / s')
+ * rounded to nearest even, both quotients exact.  The maximum is over finite
+ * elements: infinities become +-448 s', NaN stays NaN.  The first row of a block
+ * starts it afresh (whatever a recycled page held is ignored); rows behind the new
+ * ones are left as they were.  A page may receive rows of one sequence only.
+ * A position < 0, a page id outside the pool, or a scale of a block with older rows
+ * that is no power of two in range is recorded as MSA_ERR_DEVICE_ASSERT, and the
+ * rows it concerns are not written.
+ * Any of the three new tensors may be NULL, but not all (its cache and scale
+ * pointers may then be NULL).  Workspace: the status region. */
+MSA_API msa_status_t msa_append_kv_q8(const msa_params_t* params, const msa_bf16_t* k_new,
+                                      const msa_bf16_t* v_new, const msa_bf16_t* k_idx_new,
+                                      msa_e4m3_t* k, msa_e4m3_t* v, msa_e4m3_t* k_idx,
+                                      float* k_scale, float* v_scale, float* k_idx_scale,
+                                      void* workspace, size_t workspace_bytes,
+                                      msa_stream_t stream);
+
+/* Rows [token_base, token_base + n_q) of every sequence as bf16(code * scale):
+ *   k_out, v_out bf16 [batch, n_q, h, d], k_idx_out bf16 [batch, n_q, d_idx], dense,
+ * 16-byte aligned; any may be NULL, but not all.  Rows at positions >= L_b are left
+ * as they were; rows of a page outside the pool are zeros (and recorded).
+ * token_base + n_q <= max_kv.  Workspace: the status region. */
+MSA_API msa_status_t msa_read_kv_q8(const msa_params_t* params, const msa_e4m3_t* k,
+                                    const msa_e4m3_t* v, const msa_e4m3_t* k_idx,
+                                    const float* k_scale, const float* v_scale,
+                                    const float* k_idx_scale, int64_t token_base,
+                                    msa_bf16_t* k_out, msa_bf16_t* v_out, msa_bf16_t* k_idx_out,
+                                    void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* msa_block_scores over the 8-bit index key: S[beta] = k_idx_scale * max over the
+ * visible tokens of <q_idx, code>, fp32 sums.  With n_q > 1 the workspace also holds
+ * a bf16 copy of the index key (msa_workspace_size(params, MSA_OP_BLOCK_SCORES_Q8)). */
+MSA_API msa_status_t msa_block_scores_q8(const msa_params_t* params, const msa_bf16_t* q_idx,
+                                         const msa_e4m3_t* k_idx, const float* k_idx_scale,
+                                         float* block_scores, void* workspace,
+                                         size_t workspace_bytes, msa_stream_t stream);
+
+/* msa_index_select over the 8-bit index key. */
+MSA_API msa_status_t msa_index_select_q8(const msa_params_t* params, const msa_bf16_t* q_idx,
+                                         const msa_e4m3_t* k_idx, const float* k_idx_scale,
+                                         int32_t* block_ids, float* block_scores,
+                                         void* workspace, size_t workspace_bytes,
+                                         msa_stream_t stream);
+
+/* msa_sparse_attn over the 8-bit cache: softmax attention with k = k_scale * code and
+ * v = v_scale * code of the selected blocks' visible tokens; fp32 softmax and
+ * accumulation, bf16 out, the same handling of ids, empty rows and lse. */
+MSA_API msa_status_t msa_sparse_attn_q8(const msa_params_t* params, const msa_bf16_t* q,
+                                        const msa_e4m3_t* k, const msa_e4m3_t* v,
+                                        const float* k_scale, const float* v_scale,
+                                        const int32_t* block_ids, msa_bf16_t* out, float* lse,
+                                        void* workspace, size_t workspace_bytes,
+                                        msa_stream_t stream);
+
+/* msa_index_select_q8 followed by msa_sparse_attn_q8 on its ids; block_ids,
+ * block_scores and lse are optional outputs.  (A cache with 8-bit K and V and a bf16
+ * index key is served by msa_index_select and msa_sparse_attn_q8.) */
+MSA_API msa_status_t msa_forward_q8(const msa_params_t* params, const msa_bf16_t* q,
+                                    const msa_e4m3_t* k, const msa_e4m3_t* v,
+                                    const msa_bf16_t* q_idx, const msa_e4m3_t* k_idx,
+                                    const float* k_scale, const float* v_scale,
+                                    const float* k_idx_scale, msa_bf16_t* out,
+                                    int32_t* block_ids, float* block_scores, float* lse,
+                                    void* workspace, size_t workspace_bytes,
+                                    msa_stream_t stream);
 
 /* Number of kernel launches `op` makes on the stream for these shapes (its
  * plan depends on the current device's SM count); -1 on invalid params. */
