@@ -5,12 +5,20 @@
 //
 // What bounds it: L_b * d_idx bytes of HBM per sequence, half of the bf16 scan's.
 // Persistent, one CTA per SM, each an equal contiguous share of the flattened
-// (sequence, block) items.  A producer lane streams each block's codes by TMA (rows
-// of d_idx bytes, swizzled by the row size) into a ring of stages; consumer warp w
-// takes items w, w + 8, ...  A code row is read by ldmatrix as pairs of bytes: a
-// lane's 32-bit register holds four consecutive codes of one token, which two
-// hardware conversions widen to f16 pairs, i.e. to the two halves of an A fragment
-// whose 16 dims are taken in that order (the query's fragments are laid out alike).
+// (sequence, block) items; warp w takes items w, w + 8, ...  Each warp streams its own
+// items: it resolves 32 of them at a time (one per lane: sequence, block, page,
+// scale), its lane 0 issues the TMA loads (rows of d_idx bytes, swizzled by the row
+// size) into the warp's private ring of stages and refills a stage as soon as the
+// warp has read it.  One producer warp for all eight, as in the bf16 scan, issues an
+// 8 KB block every 250 ns at best: 61.7 us against NEW us for 16 x 128K tokens of 128
+// dims (41.7 us of HBM time).
+//
+// A code row is read by ldmatrix as pairs of bytes: a lane's 32-bit register holds
+// four consecutive codes of one token, which two hardware conversions widen to f16
+// pairs, i.e. to the two halves of an A fragment whose 16 dims are taken in that order
+// (the query's fragments are laid out alike).
+#include <type_traits>
+
 #include "kernels.h"
 #include "q8.cuh"
 
@@ -22,7 +30,8 @@ struct ScanQ8Args {
   int64_t qi_s0, qi_s2;
   const float* scale;
   const int32_t* seq_lens;
-  int batch, max_kv, h, block, nblk, stages;
+  int batch, max_kv, h, block, nblk;
+  int unit, depth;  // tokens per stage, stages per warp
   uint32_t stage_bytes;
   float* scores;
   int fill_tail;
@@ -31,8 +40,8 @@ struct ScanQ8Args {
   KvPages pg;
 };
 
-constexpr int kWarps = 8;      // consumer warps; one more warp produces
-constexpr int kMaxStages = 64;
+constexpr int kWarps = 8;
+constexpr int kMaxDepth = 16;  // stages of a warp
 
 __device__ __forceinline__ int seq_blocks(const ScanQ8Args& a, int b) {
   return (kv_length(a.seq_lens, b, a.max_kv, a.st) + a.block - 1) / a.block;
@@ -47,8 +56,8 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-template <int DI, int NT>
-__global__ void __launch_bounds__((kWarps + 1) * 32, 1)
+template <int DI, int NT, int MT>
+__global__ void __launch_bounds__(kWarps * 32, 1)
     index_scan_q8_kernel(const __grid_constant__ CUtensorMap tmk, ScanQ8Args a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -57,116 +66,108 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem);
-  const int S = a.stages;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)S * a.stage_bytes);
-  int4* info = reinterpret_cast<int4*>(bars + 2 * S);  // [S] (sequence, block, scale index)
-  int* n_items = reinterpret_cast<int*>(info + S);
-  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + S);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (warp == NW) {
-    // Producer warp: barriers, this CTA's share of the items (counted over the
-    // sequences' block counts), then groups of 32 items: every lane resolves one
-    // item's sequence, block and page, and lane 0 streams the group.
-    if (lane == 0) {
-      for (int s = 0; s < S; ++s) {
-        mbar_init(full0 + 8 * s, 1);
-        mbar_init(empty0 + 8 * s, 1);
-      }
-      fence_mbar_init();
-      prefetch_tensormap(&tmk);
-    }
-    const bool skip = status_failed(a.st);
-    int total = 0;
-    for (int b = lane; b < a.batch; b += 32) total += seq_blocks(a, b);
-    total = (int)__reduce_add_sync(0xffffffffu, (unsigned)total);
-    const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int i0 = (int)min((int64_t)blockIdx.x * per, (int64_t)total);
-    const int n = min(total - i0, per);
-    int b0 = 0, beta0 = 0, carry = 0;
-    bool found = false;
-    for (int base = 0; base < a.batch && !found; base += 32) {
-      const int b = base + lane;
-      const int nb = b < a.batch ? seq_blocks(a, b) : 0;
-      int inc = nb;
+  const int depth = a.depth;
+  // this warp's ring: stages, barriers, and the (sequence, block, scale) of each stage
+  const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * depth) * a.stage_bytes;
+  uint8_t* tail = smem + (size_t)(NW * depth) * a.stage_bytes;
+  int4* info = reinterpret_cast<int4*>(tail) + warp * depth;
+  const uint32_t bars =
+      smem_u32(reinterpret_cast<uint64_t*>(tail + (size_t)(NW * depth) * 16) + warp * depth);
+  if (lane == 0) {
+    for (int s = 0; s < depth; ++s) mbar_init(bars + 8 * s, 1);
+    fence_mbar_init();
+    if (warp == 0) prefetch_tensormap(&tmk);
+  }
+  const bool skip = status_failed(a.st);
+  // this CTA's share of the items, counted over the sequences' block counts
+  int total = 0;
+  for (int b = lane; b < a.batch; b += 32) total += seq_blocks(a, b);
+  total = (int)__reduce_add_sync(0xffffffffu, (unsigned)total);
+  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int i0 = (int)min((int64_t)blockIdx.x * per, (int64_t)total);
+  const int n = skip ? 0 : min(total - i0, per);
+  int b0 = 0, beta0 = 0, carry = 0;
+  bool found = false;
+  for (int base = 0; base < a.batch && !found; base += 32) {
+    const int b = base + lane;
+    const int nb = b < a.batch ? seq_blocks(a, b) : 0;
+    int inc = nb;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      const int excl = carry + inc - nb;
-      const unsigned hit = __ballot_sync(0xffffffffu, nb > 0 && i0 >= excl && i0 < excl + nb);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        b0 = base + src;
-        beta0 = i0 - __shfl_sync(0xffffffffu, excl, src);
-        found = true;
-      }
-      carry += __shfl_sync(0xffffffffu, inc, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
     }
-    if (lane == 0) *n_items = skip ? -1 : n;
-    __syncwarp();
-    named_arrive(2, (NW + 1) * 32);
-    if (skip || n == 0) return;
-    int b = b0, beta = beta0, issued = 0;
-    bool failed = false;
-    for (int k0 = 0; k0 < n && !failed; k0 += 32) {
-      int bb = b, bt = beta, tok = 0, plane = 0, sidx = 0;
-      if (k0 + lane < n) {
-        bt += lane;
-        int nbb = seq_blocks(a, bb);
-        while (bt >= nbb) {  // the item exists, so bb stays below the batch
-          bt -= nbb;
-          nbb = seq_blocks(a, ++bb);
-        }
-        kv_block_coords(a.pg, bb, bt, a.block, a.st, tok, plane);
-        sidx = a.pg.table == nullptr ? bb * a.nblk + bt : plane < a.pg.pages ? plane : -1;
-      }
-      const int cnt = min(32, n - k0);
-      for (int j = 0; j < cnt; ++j) {
-        const int tj = __shfl_sync(0xffffffffu, tok, j), pj = __shfl_sync(0xffffffffu, plane, j);
-        const int bj = __shfl_sync(0xffffffffu, bb, j), ej = __shfl_sync(0xffffffffu, bt, j);
-        const int sj = __shfl_sync(0xffffffffu, sidx, j);
-        const int k = k0 + j, s = k % S;
-        if (lane == 0 && !failed) {
-          if (k >= S &&
-              !mbar_wait_bounded(empty0 + 8 * s, ((k / S) - 1) & 1, a.st, 0x401u, a.wait_ns)) {
-            failed = true;
-          } else {
-            info[s] = make_int4(bj, ej, sj, 0);
-            const uint32_t full = full0 + 8 * s;
-            mbar_arrive_expect_tx(full, a.stage_bytes);
-            tma_load_rows(sbase + (uint32_t)s * a.stage_bytes, &tmk, full, tj, pj);
-            issued = k + 1;
-          }
-        }
-        __syncwarp();
-      }
-      failed = __shfl_sync(0xffffffffu, failed, 0);
-      b = __shfl_sync(0xffffffffu, bb, 31);  // the next group starts after this group's last item
-      beta = __shfl_sync(0xffffffffu, bt, 31) + 1;
+    const int excl = carry + inc - nb;
+    const unsigned hit = __ballot_sync(0xffffffffu, nb > 0 && i0 >= excl && i0 < excl + nb);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b0 = base + src;
+      beta0 = i0 - __shfl_sync(0xffffffffu, excl, src);
+      found = true;
     }
-    if (lane != 0) return;
-    // before leaving, wait (bounded) for the copies still in flight
-    for (int k = max(0, issued - S); k < issued; ++k)
-      mbar_wait_bounded(full0 + 8 * (k % S), (k / S) & 1, a.st, 0x403u, a.wait_ns);
-    return;
+    carry += __shfl_sync(0xffffffffu, inc, 31);
   }
 
-  named_sync(2, (NW + 1) * 32);
-  const int n = *n_items;
-  if (n < 0) return;
+  // the warp's items j = 0, 1, ...: item warp + j NW of the share
+  const int items = n > warp ? (n - warp + NW - 1) / NW : 0;
+  const int subs = a.block / a.unit;  // loads per item (1 or 2)
+  const int loads = items * subs;
+  int bb = b0, bt = beta0 + warp + lane * NW, tok = 0, plane = 0;
+  float scale = 1.f;
+  auto resolve = [&](int j) {  // this lane's item j
+    if (j >= items) return;
+    for (int nbb; bt >= (nbb = seq_blocks(a, bb)); ++bb) bt -= nbb;
+    kv_block_coords(a.pg, bb, bt, a.block, a.st, tok, plane);
+    const bool paged = a.pg.table != nullptr;
+    scale = 1.f;  // a page outside the pool reads as zeros
+    if (!paged || plane < a.pg.pages)
+      scale = __ldg(a.scale + (paged ? (int64_t)plane : (int64_t)bb * a.nblk + bt));
+  };
+  resolve(lane);
+  int is = 0;  // stage of the next load
+  auto issue = [&](int l) {
+    const int j = l / subs, sub = l - j * subs;
+    if (sub == 0 && j > 0 && (j & 31) == 0) {
+      bt += 32 * NW;
+      resolve(j + lane);
+    }
+    const int src = j & 31;
+    const int tj = __shfl_sync(0xffffffffu, tok, src), pj = __shfl_sync(0xffffffffu, plane, src);
+    const int bj = __shfl_sync(0xffffffffu, bb, src), ej = __shfl_sync(0xffffffffu, bt, src);
+    const float sj = __shfl_sync(0xffffffffu, scale, src);
+    if (lane == 0) {
+      info[is] = make_int4(bj, ej, __float_as_int(sj), 0);
+      mbar_arrive_expect_tx(bars + 8 * is, a.stage_bytes);
+      tma_load_rows(ring + (uint32_t)is * a.stage_bytes, &tmk, bars + 8 * is, tj + sub * a.unit, pj);
+    }
+    __syncwarp();
+    if (++is == depth) is = 0;
+  };
+  int issued = 0;
+  for (; issued < min(depth, loads); ++issued) issue(issued);
+
   const int r = lane >> 2, q = lane & 3;
   const float ninf = -__int_as_float(0x7f800000);
   uint32_t blo[NT][NC], bhi[NT][NC];
   float inv[NT][2];  // the query scaling of columns 2q and 2q + 1 undone
+  float cm[NT][2];
   int cur_b = -1, L = 0;
-  for (int k = warp; k < n; k += NW) {
-    const int s = k % S;
-    if (!mbar_wait_warp(full0 + 8 * s, (k / S) & 1, a.st, 0x402u, a.wait_ns)) break;
+  int s = 0, sub = 0;
+  uint32_t par = 0;
+  for (int l = 0; l < loads; ++l) {
+    if (!mbar_wait_warp(bars + 8 * s, par, a.st, 0x402u, a.wait_ns)) {
+      // before leaving, wait (bounded) for the copies still in flight
+      for (++l; l < issued; ++l) {
+        if (++s == depth) {
+          s = 0;
+          par ^= 1u;
+        }
+        mbar_wait_warp(bars + 8 * s, par, a.st, 0x403u, a.wait_ns);
+      }
+      break;
+    }
     const int4 it = info[s];
-    const float sc = it.z >= 0 ? __ldg(a.scale + it.z) : 1.f;  // a bad page reads as zeros
     if (it.x != cur_b) {
       cur_b = it.x;
       L = kv_length(a.seq_lens, cur_b, a.max_kv, a.st);
@@ -179,40 +180,67 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1)
         inv[nt][1] = __shfl_sync(0xffffffffu, f, 8 * q + 4);
       }
     }
-    const uint32_t base = sbase + (uint32_t)s * a.stage_bytes;
-    float cm[NT][2];
+    const uint32_t base = ring + (uint32_t)s * a.stage_bytes;
+    if (sub == 0) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) cm[nt][0] = cm[nt][1] = ninf;
-    for (int mt = 0; mt < a.block / 16; ++mt) {
-      float acc[NT][4];
+      for (int nt = 0; nt < NT; ++nt) cm[nt][0] = cm[nt][1] = ninf;
+    }
+    // MT 16-token tiles at a time: their MMA chains are independent
+    for (int t0 = 0; t0 < a.unit; t0 += 16 * MT) {
+      float acc[MT][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-      const uint32_t row = (uint32_t)(mt * 16 + (lane & 15));
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          acc[m][nt][0] = acc[m][nt][1] = acc[m][nt][2] = acc[m][nt][3] = 0.f;
+      const uint32_t row = (uint32_t)(t0 + (lane & 15));
 #pragma unroll
       for (int c = 0; c < NC; c += 2) {
-        uint32_t x0, x1, x2, x3;  // tokens 0-7, 8-15 of step c, then of step c + 1
-        ldmatrix_x4(base + q8::swz<DI>(row, (uint32_t)(c + (lane >> 4))), x0, x1, x2, x3);
-        const uint32_t a0 = q8::lo_f16x2(x0), a1 = q8::lo_f16x2(x1);
-        const uint32_t a2 = q8::hi_f16x2(x0), a3 = q8::hi_f16x2(x1);
-        const uint32_t b0 = q8::lo_f16x2(x2), b1 = q8::lo_f16x2(x3);
-        const uint32_t b2 = q8::hi_f16x2(x2), b3 = q8::hi_f16x2(x3);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          q8::mma_f16(acc[nt], a0, a1, a2, a3, blo[nt][c], bhi[nt][c]);
-          q8::mma_f16(acc[nt], b0, b1, b2, b3, blo[nt][c + 1], bhi[nt][c + 1]);
+        for (int m = 0; m < MT; ++m) {
+          uint32_t x0, x1, x2, x3;  // tokens 0-7, 8-15 of step c, then of step c + 1
+          ldmatrix_x4(base + q8::swz<DI>(row + 16 * m, (uint32_t)(c + (lane >> 4))), x0, x1, x2, x3);
+          const uint32_t a0 = q8::lo_f16x2(x0), a1 = q8::lo_f16x2(x1);
+          const uint32_t a2 = q8::hi_f16x2(x0), a3 = q8::hi_f16x2(x1);
+          const uint32_t b0 = q8::lo_f16x2(x2), b1 = q8::lo_f16x2(x3);
+          const uint32_t b2 = q8::hi_f16x2(x2), b3 = q8::hi_f16x2(x3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            q8::mma_f16(acc[m][nt], a0, a1, a2, a3, blo[nt][c], bhi[nt][c]);
+            q8::mma_f16(acc[m][nt], b0, b1, b2, b3, blo[nt][c + 1], bhi[nt][c + 1]);
+          }
         }
       }
-      const int jl = it.y * a.block + mt * 16 + r, jh = jl + 8;
+      const int j0 = it.y * a.block + sub * a.unit + t0;
+      if (j0 + 16 * MT <= L) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          cm[nt][e] = fmaxf(cm[nt][e], jl < L ? acc[nt][e] : ninf);
-          cm[nt][e] = fmaxf(cm[nt][e], jh < L ? acc[nt][2 + e] : ninf);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              cm[nt][e] = fmax3(cm[nt][e], acc[m][nt][e], acc[m][nt][2 + e]);
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int jl = j0 + 16 * m + r, jh = jl + 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              cm[nt][e] = fmax3(cm[nt][e], jl < L ? acc[m][nt][e] : ninf,
+                                jh < L ? acc[m][nt][2 + e] : ninf);
         }
+      }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(empty0 + 8 * s);
+    __syncwarp();  // every lane has read the stage: it may be refilled
+    if (issued < loads) issue(issued++);
+    if (++s == depth) {
+      s = 0;
+      par ^= 1u;
+    }
+    if (++sub < subs) continue;
+    sub = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -223,11 +251,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1)
         v = warp_max_xor(v, 16);
         const int g = nt * 8 + 2 * q + e;
         if (r == 0 && g < a.h)
-          a.scores[((int64_t)it.x * a.h + g) * a.nblk + it.y] = v * (inv[nt][e] * sc);
+          a.scores[((int64_t)it.x * a.h + g) * a.nblk + it.y] =
+              v * (inv[nt][e] * __int_as_float(it.z));
       }
   }
   if (a.fill_tail) {
-    // blocks past each sequence's end: -inf, spread over every consumer thread
+    // blocks past each sequence's end: -inf, spread over every thread
     const int nthr = (int)gridDim.x * NW * 32;
     const int gt = (int)blockIdx.x * NW * 32 + (int)threadIdx.x;
     for (int b = 0; b < a.batch; ++b)
@@ -236,7 +265,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 1)
   }
 }
 
-template <int DI, int NT>
+template <int DI, int NT, int MT>
 cudaError_t run_scan(const Shape& s, const uint8_t* k_idx, ScanQ8Args& a, cudaStream_t stream) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
@@ -244,7 +273,7 @@ cudaError_t run_scan(const Shape& s, const uint8_t* k_idx, ScanQ8Args& a, cudaSt
   cuuint64_t dims[3] = {(cuuint64_t)DI, (cuuint64_t)(paged ? s.block : s.max_kv),
                         (cuuint64_t)(paged ? s.pages.pages : s.batch)};
   cuuint64_t str[2] = {(cuuint64_t)s.ki_s[1], (cuuint64_t)s.ki_s[0]};
-  cuuint32_t box[3] = {DI, (cuuint32_t)s.block, 1};
+  cuuint32_t box[3] = {DI, (cuuint32_t)a.unit, 1};
   cuuint32_t es[3] = {1, 1, 1};
   CUtensorMap tmk;
   const CUtensorMapSwizzle sw = DI == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
@@ -254,18 +283,15 @@ cudaError_t run_scan(const Shape& s, const uint8_t* k_idx, ScanQ8Args& a, cudaSt
           CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  a.stage_bytes = (uint32_t)DI * (uint32_t)s.block;
-  // A stage count that is a multiple of the warps keeps each stage on one consumer
-  // warp, so a parity wait never meets a phase two fills behind.
-  const size_t fixed = 1024 + 16, per_stage = a.stage_bytes + 32;
-  const int fit = (int)(((size_t)max_smem_optin() - fixed) / per_stage);
-  a.stages = min(kMaxStages, fit - fit % kWarps);
-  if (a.stages < kWarps) return cudaErrorInvalidValue;  // 16 KB stages: 8 always fit
-  const size_t smem = fixed + (size_t)a.stages * per_stage;
-  cudaError_t err = cudaFuncSetAttribute(index_scan_q8_kernel<DI, NT>,
+  a.stage_bytes = (uint32_t)DI * (uint32_t)a.unit;
+  const size_t fixed = 1024, per_stage = a.stage_bytes + 24;
+  a.depth = min(kMaxDepth, (int)(((size_t)max_smem_optin() - fixed) / (per_stage * kWarps)));
+  if (a.depth < 1) return cudaErrorInvalidValue;  // 8 KB stages at most: 3 fit
+  const size_t smem = fixed + (size_t)(a.depth * kWarps) * per_stage;
+  cudaError_t err = cudaFuncSetAttribute(index_scan_q8_kernel<DI, NT, MT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  return launch_pdl(index_scan_q8_kernel<DI, NT>, dim3(num_sms()), dim3((kWarps + 1) * 32), smem,
+  return launch_pdl(index_scan_q8_kernel<DI, NT, MT>, dim3(num_sms()), dim3(kWarps * 32), smem,
                     stream, tmk, a);
 }
 
@@ -285,21 +311,26 @@ cudaError_t launch_index_scan_q8(const Shape& s, const uint16_t* q_idx, const ui
   a.max_kv = s.max_kv;
   a.h = s.h;
   a.block = s.block;
+  a.unit = s.block < 64 ? s.block : 64;
   a.nblk = s.nblk;
   a.scores = scores;
   a.fill_tail = fill_tail ? 1 : 0;
   a.st = st;
   a.wait_ns = 4000000000ull;
   a.pg = s.pages;
-  const bool two = s.h > 8;
-  switch (s.d_idx) {
-    case 128:
-      return two ? run_scan<128, 2>(s, k_idx, a, stream) : run_scan<128, 1>(s, k_idx, a, stream);
-    case 64:
-      return two ? run_scan<64, 2>(s, k_idx, a, stream) : run_scan<64, 1>(s, k_idx, a, stream);
-    case 32:
-      return two ? run_scan<32, 2>(s, k_idx, a, stream) : run_scan<32, 1>(s, k_idx, a, stream);
-  }
+  auto run = [&](auto di, auto nt) {
+    constexpr int DI = decltype(di)::value, NT = decltype(nt)::value;
+    return s.block >= 64   ? run_scan<DI, NT, 4>(s, k_idx, a, stream)
+           : s.block == 32 ? run_scan<DI, NT, 2>(s, k_idx, a, stream)
+                           : run_scan<DI, NT, 1>(s, k_idx, a, stream);
+  };
+  auto with_di = [&](auto di) {
+    return s.h > 8 ? run(di, std::integral_constant<int, 2>())
+                   : run(di, std::integral_constant<int, 1>());
+  };
+  if (s.d_idx == 128) return with_di(std::integral_constant<int, 128>());
+  if (s.d_idx == 64) return with_di(std::integral_constant<int, 64>());
+  if (s.d_idx == 32) return with_di(std::integral_constant<int, 32>());
   return cudaErrorInvalidValue;
 }
 

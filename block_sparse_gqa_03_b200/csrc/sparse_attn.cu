@@ -37,6 +37,8 @@
 // box per tile), codes are widened to f16 between ldmatrix and the MMA, a block's K
 // scale joins the softmax scale of its scores and its V scale the fp32 accumulation
 // of its product, so that neither is ever rounded to 16 bits.
+#include <type_traits>
+
 #include "kernels.h"
 #include "q8.cuh"
 
@@ -65,7 +67,10 @@ struct AttnArgs {
   DeviceStatus* st;
   uint64_t wait_ns;
   KvPages pg;  // table == nullptr: contiguous K/V
-  const float *ks, *vs;  // 8-bit cache: scales per (block, KV head)
+  // 8-bit cache: scales per (block, KV head); a stage holds `unit` tokens of a block,
+  // which is all of it or (block 128) half
+  const float *ks, *vs;
+  int unit;
 };
 
 constexpr float kLn2 = 0.69314718055994531f;
@@ -385,13 +390,19 @@ struct WarpStateT {
 };
 
 // ------------------------------------------------------------- 8-bit cache
-// Zeroes V rows [r0, 16) of a 16-token slice at row `tok` (codes that may be
-// uninitialised memory: a NaN code must not meet a zero probability).
+// A warp takes whole list entries (a block of one head), NS 16-token slices at a time
+// (64 tokens, fewer when the block is smaller): one running-maximum step, one
+// rescaling of O and one barrier wait serve all of them, and the slices' score
+// chains are independent.  With four warps on the slices of one entry, as for bf16,
+// the per-entry bookkeeping and the rescaling of O came to about 775 instructions
+// per slice, and the 128K decode attention took 79 us against 42 us of HBM time.
+
+// Zeroes V rows [r0, r1) (codes that may be uninitialised memory: a NaN code must not
+// meet a zero probability); the swizzle stays inside a row of D bytes.
 template <int D>
-__device__ __forceinline__ void zero_v_rows(uint8_t* vtile, int tok, int r0, int lane) {
-  constexpr int CPR = D / 16;  // 16-byte pieces per row; the swizzle stays inside a row
-  for (int x = lane; x < (16 - r0) * CPR; x += 32)
-    reinterpret_cast<uint4*>(vtile + (tok + r0) * D)[x] = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void zero_v_rows(uint8_t* vtile, int r0, int r1, int lane) {
+  for (int x = lane; x < (r1 - r0) * (D / 16); x += 32)
+    reinterpret_cast<uint4*>(vtile + r0 * D)[x] = make_uint4(0, 0, 0, 0);
 }
 
 // Four transposed codes (two tokens x two neighbouring dims, as ldmatrix.trans
@@ -403,9 +414,10 @@ __device__ __forceinline__ uint32_t by_dim(uint32_t v) { return __byte_perm(v, 0
 // in the order 4j, 4j + 1, 4j + 2, 4j + 3 per lane quad j and the query fragments
 // follow it; a transposed V register holds two dims of two tokens, so output row r
 // of tile mt is dim 16mt + 2r and row r + 8 dim 16mt + 2r + 1.
-template <int D>
+template <int D, int NS_>
 struct WarpStateTQ {
   static constexpr bool kQ8 = true;
+  static constexpr int kD = D, NS = NS_;
   uint32_t qlo[D / 16], qhi[D / 16];
   float o[D / 16][4];
   float m0, m1, l0, l1;
@@ -428,65 +440,89 @@ struct WarpStateTQ {
     f1 = __shfl_sync(0xffffffffu, inv, 8 * q4 + 4);
   }
 
+  // 16 NS tokens: rows `tok`.. of the tiles, absolute first token j0 < lim.
   __device__ __forceinline__ void attend(uint8_t* smem, uint32_t sbase, uint32_t kbase,
                                          uint32_t vbase, int tok, int j0, int lim, int lane,
                                          float ks, float vs, bool& wrote_smem) {
     const int r = lane >> 2;
     const float ninf = neg_inf();
-    if (j0 + 16 > lim) {
-      zero_v_rows<D>(smem + (vbase - sbase), tok, lim - j0, lane);
+    const bool cut = j0 + 16 * NS > lim;
+    if (cut) {
+      zero_v_rows<D>(smem + (vbase - sbase), tok + lim - j0, tok + 16 * NS, lane);
       wrote_smem = true;
       __syncwarp();
     }
-    // tokens tok + lane % 16, chunks c (lanes 0-15) and c + 1
+    // tokens tok + 16u + lane % 16, chunks c (lanes 0-15) and c + 1
     const uint32_t row = tok + (lane & 15);
-    // S^T: tokens tok + r (s[0], s[1]) and tok + r + 8 (s[2], s[3]), heads 2q4, 2q4 + 1;
-    // two accumulators halve the chain of dependent MMAs
-    float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+    // S^T of slice u: tokens 16u + r (s[0], s[1]) and 16u + r + 8 (s[2], s[3]), heads
+    // 2q4, 2q4 + 1
+    float s[NS][4];
+#pragma unroll
+    for (int u = 0; u < NS; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 16; c += 2) {
-      uint32_t k0, k1, k2, k3;  // tokens 0-7, 8-15 of step c, then of step c + 1
-      ldmatrix_x4(kbase + q8::swz<D>(row, c + (lane >> 4)), k0, k1, k2, k3);
-      q8::mma_f16(s, q8::lo_f16x2(k0), q8::lo_f16x2(k1), q8::hi_f16x2(k0), q8::hi_f16x2(k1),
-                  qlo[c], qhi[c]);
-      q8::mma_f16(t, q8::lo_f16x2(k2), q8::lo_f16x2(k3), q8::hi_f16x2(k2), q8::hi_f16x2(k3),
-                  qlo[c + 1], qhi[c + 1]);
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+        uint32_t k0, k1, k2, k3;  // tokens 0-7, 8-15 of step c, then of step c + 1
+        ldmatrix_x4(kbase + q8::swz<D>(row + 16 * u, c + (lane >> 4)), k0, k1, k2, k3);
+        q8::mma_f16(s[u], q8::lo_f16x2(k0), q8::lo_f16x2(k1), q8::hi_f16x2(k0), q8::hi_f16x2(k1),
+                    qlo[c], qhi[c]);
+        q8::mma_f16(s[u], q8::lo_f16x2(k2), q8::lo_f16x2(k3), q8::hi_f16x2(k2), q8::hi_f16x2(k3),
+                    qlo[c + 1], qhi[c + 1]);
+      }
     }
     const float g0 = f0 * ks, g1 = f1 * ks;
-    const bool ok_lo = j0 + r < lim, ok_hi = j0 + r + 8 < lim;
-    s[0] = ok_lo ? (s[0] + t[0]) * g0 : ninf;
-    s[1] = ok_lo ? (s[1] + t[1]) * g1 : ninf;
-    s[2] = ok_hi ? (s[2] + t[2]) * g0 : ninf;
-    s[3] = ok_hi ? (s[3] + t[3]) * g1 : ninf;
-    float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+    float mx0 = ninf, mx1 = ninf;
+#pragma unroll
+    for (int u = 0; u < NS; ++u) {
+      mul2(s[u][0], s[u][1], s[u][0], s[u][1], g0, g1);
+      mul2(s[u][2], s[u][3], s[u][2], s[u][3], g0, g1);
+      if (cut) {
+        const int j = j0 + 16 * u + r;
+        s[u][0] = j < lim ? s[u][0] : ninf;
+        s[u][1] = j < lim ? s[u][1] : ninf;
+        s[u][2] = j + 8 < lim ? s[u][2] : ninf;
+        s[u][3] = j + 8 < lim ? s[u][3] : ninf;
+      }
+      mx0 = fmax3(mx0, s[u][0], s[u][2]);
+      mx1 = fmax3(mx1, s[u][1], s[u][3]);
+    }
     mx0 = warp_max_xor(warp_max_xor(warp_max_xor(mx0, 4), 8), 16);
     mx1 = warp_max_xor(warp_max_xor(warp_max_xor(mx1, 4), 8), 16);
     const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-    const float c0 = exp2f(m0 - mn0), c1 = exp2f(m1 - mn1);
+    const float c0 = exp2_approx(m0 - mn0), c1 = exp2_approx(m1 - mn1);
     m0 = mn0;
     m1 = mn1;
-    s[0] = exp2f(s[0] - mn0);
-    s[1] = exp2f(s[1] - mn1);
-    s[2] = exp2f(s[2] - mn0);
-    s[3] = exp2f(s[3] - mn1);
-    l0 = l0 * c0 + (s[0] + s[2]);
-    l1 = l1 * c1 + (s[1] + s[3]);
-    // probabilities in [0, 1] as f16 (relative error 2^-12, absolute 2^-25 below 2^-14)
-    const uint32_t pb0 = movmatrix_trans(q8::pack_f16(s[0], s[1]));
-    const uint32_t pb1 = movmatrix_trans(q8::pack_f16(s[2], s[3]));
+    mul2(l0, l1, l0, l1, c0, c1);
+    // probabilities in [0, 1] as f16 (relative error 2^-11, absolute 2^-25 below 2^-14)
+    uint32_t pb[NS][2];
+#pragma unroll
+    for (int u = 0; u < NS; ++u) {
+      add2(s[u][0], s[u][1], s[u][0], s[u][1], -mn0, -mn1);
+      add2(s[u][2], s[u][3], s[u][2], s[u][3], -mn0, -mn1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[u][e] = exp2_approx(s[u][e]);
+      add2(l0, l1, l0, l1, s[u][0], s[u][1]);
+      add2(l0, l1, l0, l1, s[u][2], s[u][3]);
+      pb[u][0] = movmatrix_trans(q8::pack_f16(s[u][0], s[u][1]));
+      pb[u][1] = movmatrix_trans(q8::pack_f16(s[u][2], s[u][3]));
+    }
 #pragma unroll
     for (int mt = 0; mt < D / 16; mt += 2) {
-      uint32_t v0, v1, v2, v3;  // tokens 0-7, 8-15 of dims 16mt.., then of the next 16
-      ldmatrix_x4_trans(vbase + q8::swz<D>(row, mt + (lane >> 4)), v0, v1, v2, v3);
-      v0 = by_dim(v0);
-      v1 = by_dim(v1);
-      v2 = by_dim(v2);
-      v3 = by_dim(v3);
-      float x[4], y[4];
-      q8::mma_f16_zero(x, q8::lo_f16x2(v0), q8::hi_f16x2(v0), q8::lo_f16x2(v1), q8::hi_f16x2(v1),
-                       pb0, pb1);
-      q8::mma_f16_zero(y, q8::lo_f16x2(v2), q8::hi_f16x2(v2), q8::lo_f16x2(v3), q8::hi_f16x2(v3),
-                       pb0, pb1);
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+        uint32_t v0, v1, v2, v3;  // tokens 0-7, 8-15 of dims 16mt.., then of the next 16
+        ldmatrix_x4_trans(vbase + q8::swz<D>(row + 16 * u, mt + (lane >> 4)), v0, v1, v2, v3);
+        v0 = by_dim(v0);
+        v1 = by_dim(v1);
+        v2 = by_dim(v2);
+        v3 = by_dim(v3);
+        q8::mma_f16(x, q8::lo_f16x2(v0), q8::hi_f16x2(v0), q8::lo_f16x2(v1), q8::hi_f16x2(v1),
+                    pb[u][0], pb[u][1]);
+        q8::mma_f16(y, q8::lo_f16x2(v2), q8::hi_f16x2(v2), q8::lo_f16x2(v3), q8::hi_f16x2(v3),
+                    pb[u][0], pb[u][1]);
+      }
       // o = o c + vs x
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
@@ -528,9 +564,10 @@ struct WarpStateTQ {
 // WarpState over an 8-bit cache (up to 16 heads on the MMA rows).  Output tile
 // columns: for dims 16c .. 16c + 15, o[2c] holds the even dims and o[2c + 1] the odd
 // ones (column n is dim 16c + 2n (+ 1)).
-template <int D>
+template <int D, int NS_>
 struct WarpStateQ {
   static constexpr bool kQ8 = true;
+  static constexpr int kD = D, NS = NS_;
   uint32_t qlo[2][D / 16], qhi[2][D / 16];  // head rows r and r + 8
   float o[D / 8][4];
   float m_a, m_b, l_a, l_b;
@@ -558,85 +595,94 @@ struct WarpStateQ {
                                          float ks, float vs, bool& wrote_smem) {
     const int q4 = lane & 3;
     const float ninf = neg_inf();
-    if (j0 + 16 > lim) {
-      zero_v_rows<D>(smem + (vbase - sbase), tok, lim - j0, lane);
+    const bool cut = j0 + 16 * NS > lim;
+    if (cut) {
+      zero_v_rows<D>(smem + (vbase - sbase), tok + lim - j0, tok + 16 * NS, lane);
       wrote_smem = true;
       __syncwarp();
     }
     const uint32_t row = tok + (lane & 15);
-    float sc[2][4];
+    float sc[2 * NS][4];  // 8-token columns
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+    for (int nt = 0; nt < 2 * NS; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
 #pragma unroll
     for (int c = 0; c < D / 16; c += 2) {
-      uint32_t k0, k1, k2, k3;  // tokens 0-7, 8-15 of step c, then of step c + 1
-      ldmatrix_x4(kbase + q8::swz<D>(row, c + (lane >> 4)), k0, k1, k2, k3);
-      q8::mma_f16(sc[0], qlo[0][c], qlo[1][c], qhi[0][c], qhi[1][c], q8::lo_f16x2(k0),
-                  q8::hi_f16x2(k0));
-      q8::mma_f16(sc[1], qlo[0][c], qlo[1][c], qhi[0][c], qhi[1][c], q8::lo_f16x2(k1),
-                  q8::hi_f16x2(k1));
-      q8::mma_f16(sc[0], qlo[0][c + 1], qlo[1][c + 1], qhi[0][c + 1], qhi[1][c + 1],
-                  q8::lo_f16x2(k2), q8::hi_f16x2(k2));
-      q8::mma_f16(sc[1], qlo[0][c + 1], qlo[1][c + 1], qhi[0][c + 1], qhi[1][c + 1],
-                  q8::lo_f16x2(k3), q8::hi_f16x2(k3));
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+        uint32_t k0, k1, k2, k3;  // tokens 0-7, 8-15 of step c, then of step c + 1
+        ldmatrix_x4(kbase + q8::swz<D>(row + 16 * u, c + (lane >> 4)), k0, k1, k2, k3);
+        q8::mma_f16(sc[2 * u], qlo[0][c], qlo[1][c], qhi[0][c], qhi[1][c], q8::lo_f16x2(k0),
+                    q8::hi_f16x2(k0));
+        q8::mma_f16(sc[2 * u + 1], qlo[0][c], qlo[1][c], qhi[0][c], qhi[1][c], q8::lo_f16x2(k1),
+                    q8::hi_f16x2(k1));
+        q8::mma_f16(sc[2 * u], qlo[0][c + 1], qlo[1][c + 1], qhi[0][c + 1], qhi[1][c + 1],
+                    q8::lo_f16x2(k2), q8::hi_f16x2(k2));
+        q8::mma_f16(sc[2 * u + 1], qlo[0][c + 1], qlo[1][c + 1], qhi[0][c + 1], qhi[1][c + 1],
+                    q8::lo_f16x2(k3), q8::hi_f16x2(k3));
+      }
     }
     const float g_a = f_a * ks, g_b = f_b * ks;
     float mx_a = ninf, mx_b = ninf;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool ok = j0 + nt * 8 + 2 * q4 + e < lim;
-        sc[nt][e] = ok ? sc[nt][e] * g_a : ninf;
-        sc[nt][2 + e] = ok ? sc[nt][2 + e] * g_b : ninf;
-        mx_a = fmaxf(mx_a, sc[nt][e]);
-        mx_b = fmaxf(mx_b, sc[nt][2 + e]);
+    for (int nt = 0; nt < 2 * NS; ++nt) {
+      mul2(sc[nt][0], sc[nt][1], sc[nt][0], sc[nt][1], g_a, g_a);
+      mul2(sc[nt][2], sc[nt][3], sc[nt][2], sc[nt][3], g_b, g_b);
+      if (cut) {
+        const int j = j0 + nt * 8 + 2 * q4;
+        sc[nt][0] = j < lim ? sc[nt][0] : ninf;
+        sc[nt][1] = j + 1 < lim ? sc[nt][1] : ninf;
+        sc[nt][2] = j < lim ? sc[nt][2] : ninf;
+        sc[nt][3] = j + 1 < lim ? sc[nt][3] : ninf;
       }
+      mx_a = fmax3(mx_a, sc[nt][0], sc[nt][1]);
+      mx_b = fmax3(mx_b, sc[nt][2], sc[nt][3]);
+    }
     mx_a = warp_max_xor(warp_max_xor(mx_a, 1), 2);
     mx_b = warp_max_xor(warp_max_xor(mx_b, 1), 2);
     const float mn_a = fmaxf(m_a, mx_a), mn_b = fmaxf(m_b, mx_b);
-    const float c_a = exp2f(m_a - mn_a), c_b = exp2f(m_b - mn_b);
+    const float c_a = exp2_approx(m_a - mn_a), c_b = exp2_approx(m_b - mn_b);
     m_a = mn_a;
     m_b = mn_b;
     float ps_a = 0.f, ps_b = 0.f;
+    uint32_t pa[NS][4];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sc[nt][e] = exp2f(sc[nt][e] - mn_a);
-        sc[nt][2 + e] = exp2f(sc[nt][2 + e] - mn_b);
-        ps_a += sc[nt][e];
-        ps_b += sc[nt][2 + e];
-      }
+    for (int nt = 0; nt < 2 * NS; ++nt) {
+      const float p0 = exp2_approx(sc[nt][0] - mn_a), p1 = exp2_approx(sc[nt][1] - mn_a);
+      const float p2 = exp2_approx(sc[nt][2] - mn_b), p3 = exp2_approx(sc[nt][3] - mn_b);
+      ps_a += p0 + p1;
+      ps_b += p2 + p3;
+      pa[nt / 2][(nt & 1) * 2] = q8::pack_f16(p0, p1);
+      pa[nt / 2][(nt & 1) * 2 + 1] = q8::pack_f16(p2, p3);
+    }
     l_a = l_a * c_a + ps_a;
     l_b = l_b * c_b + ps_b;
-    const uint32_t pa0 = q8::pack_f16(sc[0][0], sc[0][1]);
-    const uint32_t pa1 = q8::pack_f16(sc[0][2], sc[0][3]);
-    const uint32_t pa2 = q8::pack_f16(sc[1][0], sc[1][1]);
-    const uint32_t pa3 = q8::pack_f16(sc[1][2], sc[1][3]);
     auto add = [&](float (&acc)[4], const float (&x)[4]) {
-      acc[0] = fmaf(vs, x[0], acc[0] * c_a);
-      acc[1] = fmaf(vs, x[1], acc[1] * c_a);
-      acc[2] = fmaf(vs, x[2], acc[2] * c_b);
-      acc[3] = fmaf(vs, x[3], acc[3] * c_b);
+      mul2(acc[0], acc[1], acc[0], acc[1], c_a, c_a);
+      fma2(acc[0], acc[1], x[0], x[1], vs, vs, acc[0], acc[1]);
+      mul2(acc[2], acc[3], acc[2], acc[3], c_b, c_b);
+      fma2(acc[2], acc[3], x[2], x[3], vs, vs, acc[2], acc[3]);
     };
 #pragma unroll
     for (int c = 0; c < D / 16; c += 2) {
-      uint32_t v0, v1, v2, v3;  // tokens 0-7, 8-15 of dims 16c.., then of the next 16
-      ldmatrix_x4_trans(vbase + q8::swz<D>(row, c + (lane >> 4)), v0, v1, v2, v3);
-      v0 = by_dim(v0);
-      v1 = by_dim(v1);
-      v2 = by_dim(v2);
-      v3 = by_dim(v3);
-      float x[4];
-      q8::mma_f16_zero(x, pa0, pa1, pa2, pa3, q8::lo_f16x2(v0), q8::lo_f16x2(v1));
-      add(o[2 * c], x);
-      q8::mma_f16_zero(x, pa0, pa1, pa2, pa3, q8::hi_f16x2(v0), q8::hi_f16x2(v1));
-      add(o[2 * c + 1], x);
-      q8::mma_f16_zero(x, pa0, pa1, pa2, pa3, q8::lo_f16x2(v2), q8::lo_f16x2(v3));
-      add(o[2 * c + 2], x);
-      q8::mma_f16_zero(x, pa0, pa1, pa2, pa3, q8::hi_f16x2(v2), q8::hi_f16x2(v3));
-      add(o[2 * c + 3], x);
+      float x[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+        uint32_t v0, v1, v2, v3;  // tokens 0-7, 8-15 of dims 16c.., then of the next 16
+        ldmatrix_x4_trans(vbase + q8::swz<D>(row + 16 * u, c + (lane >> 4)), v0, v1, v2, v3);
+        v0 = by_dim(v0);
+        v1 = by_dim(v1);
+        v2 = by_dim(v2);
+        v3 = by_dim(v3);
+        const uint32_t(&p)[4] = pa[u];
+        q8::mma_f16(x[0], p[0], p[1], p[2], p[3], q8::lo_f16x2(v0), q8::lo_f16x2(v1));
+        q8::mma_f16(x[1], p[0], p[1], p[2], p[3], q8::hi_f16x2(v0), q8::hi_f16x2(v1));
+        q8::mma_f16(x[2], p[0], p[1], p[2], p[3], q8::lo_f16x2(v2), q8::lo_f16x2(v3));
+        q8::mma_f16(x[3], p[0], p[1], p[2], p[3], q8::hi_f16x2(v2), q8::hi_f16x2(v3));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add(o[2 * c + i], x[i]);
     }
   }
 
@@ -677,6 +723,70 @@ __device__ __forceinline__ void entry_scales(const AttnArgs& a, int beta, int pl
   ks = plane < 0 ? 1.f : __ldg(a.ks + at);
   vs = plane < 0 ? 1.f : __ldg(a.vs + at);
 }
+
+// A consumer warp's way through the items of an 8-bit cache (item = `unit` tokens of a
+// list entry): items warp, warp + nw, ..., item i in stage i % stages, nw = min(NC,
+// stages).  A stage's successive fills belong to different warps, so a warp first
+// makes sure that the fill before its own has been consumed: the parity test of the
+// full barrier could otherwise meet the fill before that one.  (The test of the empty
+// barrier cannot be that far off: the warp's previous item was only issued after the
+// fill two before this one had been consumed, since stages >= nw.)
+template <int NC>
+struct Q8Walk {
+  int i, s, fill;  // item, stage, how often the stage was filled before
+  int nw, n;       // stride, items
+  int shift;       // log2 of the items per entry
+  float ks, vs, ks_n, vs_n;
+
+  __device__ __forceinline__ void start(const AttnArgs& a, int warp, int entries,
+                                        const int32_t* list, const int32_t* plist,
+                                        const int32_t* glist) {
+    nw = min(NC, a.stages);
+    shift = a.unit < a.block ? 1 : 0;
+    n = warp < nw ? entries << shift : 0;
+    i = s = warp;
+    fill = 0;
+    ks_n = vs_n = 1.f;
+    fetch(a, i, list, plist, glist);
+  }
+  __device__ __forceinline__ void fetch(const AttnArgs& a, int item, const int32_t* list,
+                                        const int32_t* plist, const int32_t* glist) {
+    const int e = item >> shift;
+    if (item < n) entry_scales(a, list[e] & 0xffff, plist[e], glist[e], ks_n, vs_n);
+  }
+  // Waits for item i (false: a wait ran out) and requests the next one's scales.
+  __device__ __forceinline__ bool wait(const AttnArgs& a, uint32_t full0, uint32_t empty0,
+                                       const int32_t* list, const int32_t* plist,
+                                       const int32_t* glist) {
+    ks = ks_n;
+    vs = vs_n;
+    fetch(a, i + nw, list, plist, glist);
+    if (fill > 0 && !mbar_wait_warp(empty0 + 8 * s, (fill - 1) & 1, a.st, 4u, a.wait_ns))
+      return false;
+    return mbar_wait_warp(full0 + 8 * s, fill & 1, a.st, 3u, a.wait_ns);
+  }
+  // Attends to item i (list entry e) and releases its stage.
+  template <class WS>
+  __device__ __forceinline__ void attend(const AttnArgs& a, WS& ws, uint8_t* smem, uint32_t sbase,
+                                         uint32_t empty0, int e, int lim, int lane) {
+    const uint32_t kbase = sbase + (uint32_t)s * a.stage_bytes;
+    const int j0 = (e & 0xffff) * a.block + (i & ((1 << shift) - 1)) * a.unit;
+    bool wrote = false;
+    for (int t = 0; t < a.unit && j0 + t < lim; t += 16 * WS::NS)
+      ws.attend(smem, sbase, kbase, kbase + WS::kD * a.unit, t, j0 + t, lim, lane, ks, vs, wrote);
+    if (wrote) fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty0 + 8 * s);
+  }
+  __device__ __forceinline__ void next(int stages) {
+    i += nw;
+    s += nw;
+    if (s >= stages) {
+      s -= stages;
+      ++fill;
+    }
+  }
+};
 
 // Merge of NC warp states for tile row `row`, dims [dim, dim + 4) (dim a
 // multiple of 4): normalised output and natural-log LSE (-inf and 0 when no key
@@ -730,7 +840,7 @@ __device__ __forceinline__ void consumer_sync(int nthreads) {
 // Each entry is (block id in the low 16 bits, row offset in the high bits); the
 // row supplies the sequence and the KV head.  Waits are bounded; before leaving,
 // the producer waits for its copies still in flight.
-template <int D, bool Q8 = false>
+template <int D>
 __device__ __forceinline__ void produce(const AttnArgs& a, const CUtensorMap* tmk,
                                         const CUtensorMap* tmv, const int32_t* list,
                                         const int32_t* plist, const int32_t* glist, int n,
@@ -766,18 +876,50 @@ __device__ __forceinline__ void produce(const AttnArgs& a, const CUtensorMap* tm
     const uint32_t full = full0 + 8 * s;
     mbar_arrive_expect_tx(full, a.stage_bytes);
     const uint32_t kdst = sbase + (uint32_t)s * a.stage_bytes;
-    if constexpr (Q8) {
-      tma_load_4d(kdst, tmk, full, 0, g, tok, plane);
-      tma_load_4d(kdst + D * a.block, tmv, full, 0, g, tok, plane);
-    } else {
-      const uint32_t vdst = kdst + NH * half_bytes;
+    const uint32_t vdst = kdst + NH * half_bytes;
 #pragma unroll
-      for (int hh = 0; hh < NH; ++hh) {
-        tma_load_4d(kdst + hh * half_bytes, tmk, full, hh * 64, g, tok, plane);
-        tma_load_4d(vdst + hh * half_bytes, tmv, full, hh * 64, g, tok, plane);
-      }
+    for (int hh = 0; hh < NH; ++hh) {
+      tma_load_4d(kdst + hh * half_bytes, tmk, full, hh * 64, g, tok, plane);
+      tma_load_4d(vdst + hh * half_bytes, tmv, full, hh * 64, g, tok, plane);
     }
     ++issued;
+  }
+  for (int i = max(0, issued - a.stages); i < issued; ++i)
+    mbar_wait_bounded(full0 + 8 * (i % a.stages), (i / a.stages) & 1, a.st, 2u, a.wait_ns);
+}
+
+// The same for an 8-bit cache: items of `unit` tokens, one box for K and one for V.
+template <int D>
+__device__ __forceinline__ void produce_q8(const AttnArgs& a, const CUtensorMap* tmk,
+                                           const CUtensorMap* tmv, const int32_t* list,
+                                           const int32_t* plist, const int32_t* glist, int n,
+                                           uint32_t sbase, uint32_t full0, uint32_t empty0) {
+  prefetch_tensormap(tmk);
+  prefetch_tensormap(tmv);
+  int s = 0, fill = 0, issued = 0;
+  bool ok = true;
+  for (int i = 0; i < n && ok; ++i) {
+    const int g = glist[i], p = plist[i];
+    const bool paged = a.pg.table != nullptr;
+    const int plane = paged && p < 0 ? (int)a.pg.pages : p;
+    const int tok = paged ? 0 : (list[i] & 0xffff) * a.block;
+    for (int t = 0; t < a.block; t += a.unit) {
+      if (fill > 0 &&
+          !mbar_wait_bounded(empty0 + 8 * s, (fill - 1) & 1, a.st, 1u, a.wait_ns)) {
+        ok = false;
+        break;
+      }
+      const uint32_t full = full0 + 8 * s;
+      mbar_arrive_expect_tx(full, a.stage_bytes);
+      const uint32_t kdst = sbase + (uint32_t)s * a.stage_bytes;
+      tma_load_4d(kdst, tmk, full, 0, g, tok + t, plane);
+      tma_load_4d(kdst + D * a.unit, tmv, full, 0, g, tok + t, plane);
+      ++issued;
+      if (++s == a.stages) {
+        s = 0;
+        ++fill;
+      }
+    }
   }
   for (int i = max(0, issued - a.stages); i < issued; ++i)
     mbar_wait_bounded(full0 + 8 * (i % a.stages), (i / a.stages) & 1, a.st, 2u, a.wait_ns);
@@ -873,7 +1015,7 @@ __global__ void __launch_bounds__(5 * 32, 1)
   if (tid == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, min(NC, nsub));
+      mbar_init(empty0 + 8 * s, WS::kQ8 ? 1 : min(NC, nsub));
     }
     fence_mbar_init();
   }
@@ -894,39 +1036,40 @@ __global__ void __launch_bounds__(5 * 32, 1)
   const int n = *n_list;
   if (n < 0) return;
   if (warp == NC) {
-    if (lane == 0 && n > 0)
-      produce<D, WS::kQ8>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
+    if (lane == 0 && n > 0) {
+      if constexpr (WS::kQ8)
+        produce_q8<D>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
+      else
+        produce<D>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
+    }
     return;
   }
-  const int step = nsub >= NC ? 1 : NC / nsub;  // a warp takes every step-th entry
-  float ks_n = 1.f, vs_n = 1.f;                 // scales of this warp's next entry
-  auto next_scales = [&](int i) {
-    if (WS::kQ8 && i < n) entry_scales(a, list[i] & 0xffff, plist[i], glist[i], ks_n, vs_n);
-  };
-  next_scales(nsub >= NC ? 0 : warp / nsub);
-  for (int i = 0; i < n; ++i) {
-    const int u0 = i * nsub;
-    const int st0 = (warp - (u0 % NC) + NC) % NC;  // first slice of block i owned by this warp
-    if (st0 >= nsub) continue;
-    const int s = i % a.stages;
-    const float ks = ks_n, vs = vs_n;
-    next_scales(i + step);
-    if (!mbar_wait_warp(full0 + 8 * s, (i / a.stages) & 1, a.st, 3u, a.wait_ns)) break;
-    const uint32_t kbase = sbase + (uint32_t)s * a.stage_bytes;
-    const uint32_t vbase = kbase + (WS::kQ8 ? D * a.block : (D / 64) * half_bytes);
-    const int beta = list[i] & 0xffff;
-    bool wrote = false;
-    for (int st = st0; st < nsub; st += NC) {
-      const int j0 = beta * a.block + st * 16;
-      if (j0 >= rg.lim) continue;
-      if constexpr (WS::kQ8)
-        ws.attend(smem, sbase, kbase, vbase, st * 16, j0, rg.lim, lane, ks, vs, wrote);
-      else
-        ws.attend(a, smem, sbase, kbase, vbase, half_bytes, st * 16, j0, rg.lim, lane, wrote);
+  if constexpr (WS::kQ8) {
+    Q8Walk<NC> w;
+    for (w.start(a, warp, n, list, plist, glist); w.i < w.n; w.next(a.stages)) {
+      if (!w.wait(a, full0, empty0, list, plist, glist)) break;
+      w.attend(a, ws, smem, sbase, empty0, list[w.i >> w.shift], rg.lim, lane);
     }
-    if (wrote) fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(empty0 + 8 * s);
+  } else {
+    for (int i = 0; i < n; ++i) {
+      const int u0 = i * nsub;
+      const int st0 = (warp - (u0 % NC) + NC) % NC;  // first slice of block i owned by this warp
+      if (st0 >= nsub) continue;
+      const int s = i % a.stages;
+      if (!mbar_wait_warp(full0 + 8 * s, (i / a.stages) & 1, a.st, 3u, a.wait_ns)) break;
+      const uint32_t kbase = sbase + (uint32_t)s * a.stage_bytes;
+      const uint32_t vbase = kbase + (D / 64) * half_bytes;
+      const int beta = list[i] & 0xffff;
+      bool wrote = false;
+      for (int st = st0; st < nsub; st += NC) {
+        const int j0 = beta * a.block + st * 16;
+        if (j0 < rg.lim)
+          ws.attend(a, smem, sbase, kbase, vbase, half_bytes, st * 16, j0, rg.lim, lane, wrote);
+      }
+      if (wrote) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8 * s);
+    }
   }
   // Merge the warps' states (the stages are free: every load was consumed).
   consumer_sync(NC * 32);
@@ -984,7 +1127,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     if (lane == 0) {
       for (int s = 0; s < a.stages; ++s) {
         mbar_init(full0 + 8 * s, 1);
-        mbar_init(empty0 + 8 * s, min(NC, nsub));
+        mbar_init(empty0 + 8 * s, WS::kQ8 ? 1 : min(NC, nsub));
       }
       fence_mbar_init();
     }
@@ -993,8 +1136,12 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     if (lane == 0) *n_list = skip ? -1 : n;
     __syncwarp();
     named_arrive(2, (NC + 1) * 32);
-    if (lane == 0 && !skip && n > 0)
-      produce<D, WS::kQ8>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
+    if (lane == 0 && !skip && n > 0) {
+      if constexpr (WS::kQ8)
+        produce_q8<D>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
+      else
+        produce<D>(a, &tmk, &tmv, list, plist, glist, n, sbase, full0, empty0);
+    }
     return;
   }
   // the consumers load their first row's queries while the list is built
@@ -1172,15 +1319,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
     consumer_sync(NC * 32);  // the merge buffer is free again
   };
 
-  const int step = nsub >= NC ? 1 : NC / nsub;  // a warp takes every step-th entry
-  float ks_n = 1.f, vs_n = 1.f;                 // scales of this warp's next entry
-  auto next_scales = [&](int i) {
-    if (WS::kQ8 && i < n) entry_scales(a, list[i] & 0xffff, plist[i], glist[i], ks_n, vs_n);
-  };
-  next_scales(nsub >= NC ? 0 : warp / nsub);
-  for (int i = 0; i < n; ++i) {
-    const int e = list[i];
-    const int64_t row = r0 + (e >> 16);
+  // Moves on to `row`: ends the rows before it.
+  auto go_to = [&](int64_t row) {
     while (cur < row) {
       flush();
       ++cur;
@@ -1188,33 +1328,46 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
       ws.reset();
       ws.load_q(a, rg, lane);
     }
-    const int u0 = i * nsub;
-    const int st0 = (warp - (u0 % NC) + NC) % NC;
-    if (st0 >= nsub || failed) continue;
-    const int s = i % a.stages;
-    const float ks = ks_n, vs = vs_n;
-    next_scales(i + step);
-    // After a wait runs out this warp stops computing but keeps walking the list,
-    // so that every consumer warp still reaches the same row-boundary barriers.
-    if (!mbar_wait_warp(full0 + 8 * s, (i / a.stages) & 1, a.st, 3u, a.wait_ns)) {
-      failed = true;
-      continue;
+  };
+  if constexpr (WS::kQ8) {
+    Q8Walk<NC> w;
+    for (w.start(a, warp, n, list, plist, glist); w.i < w.n; w.next(a.stages)) {
+      const int e = list[w.i >> w.shift];
+      go_to(r0 + (e >> 16));
+      // after a wait runs out the warp computes no more but keeps walking (see below)
+      if (failed || !w.wait(a, full0, empty0, list, plist, glist)) {
+        failed = true;
+        continue;
+      }
+      w.attend(a, ws, smem, sbase, empty0, e, rg.lim, lane);
     }
-    const uint32_t kbase = sbase + (uint32_t)s * a.stage_bytes;
-    const uint32_t vbase = kbase + (WS::kQ8 ? D * a.block : (D / 64) * half_bytes);
-    const int beta = e & 0xffff;
-    bool wrote = false;
-    for (int st = st0; st < nsub; st += NC) {
-      const int j0 = beta * a.block + st * 16;
-      if (j0 >= rg.lim) continue;
-      if constexpr (WS::kQ8)
-        ws.attend(smem, sbase, kbase, vbase, st * 16, j0, rg.lim, lane, ks, vs, wrote);
-      else
-        ws.attend(a, smem, sbase, kbase, vbase, half_bytes, st * 16, j0, rg.lim, lane, wrote);
+  } else {
+    for (int i = 0; i < n; ++i) {
+      const int e = list[i];
+      go_to(r0 + (e >> 16));
+      const int u0 = i * nsub;
+      const int st0 = (warp - (u0 % NC) + NC) % NC;
+      if (st0 >= nsub || failed) continue;
+      const int s = i % a.stages;
+      // After a wait runs out this warp stops computing but keeps walking the list,
+      // so that every consumer warp still reaches the same row-boundary barriers.
+      if (!mbar_wait_warp(full0 + 8 * s, (i / a.stages) & 1, a.st, 3u, a.wait_ns)) {
+        failed = true;
+        continue;
+      }
+      const uint32_t kbase = sbase + (uint32_t)s * a.stage_bytes;
+      const uint32_t vbase = kbase + (D / 64) * half_bytes;
+      const int beta = e & 0xffff;
+      bool wrote = false;
+      for (int st = st0; st < nsub; st += NC) {
+        const int j0 = beta * a.block + st * 16;
+        if (j0 < rg.lim)
+          ws.attend(a, smem, sbase, kbase, vbase, half_bytes, st * 16, j0, rg.lim, lane, wrote);
+      }
+      if (wrote) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8 * s);
     }
-    if (wrote) fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(empty0 + 8 * s);
   }
   while (true) {
     flush();
@@ -1226,6 +1379,10 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
 }
 
 // ------------------------------------------------------------ host helpers
+// Tokens per stage of an 8-bit cache: 16 KB at most, so that there are more stages
+// than consumer warps.
+int q8_unit(const Shape& s) { return s.block < 64 ? s.block : 64; }
+
 // K or V as a 4-D tensor [batch][token][kv head][dim], or for a paged cache
 // [page][token in page][kv head][dim]; one box is 64 dims x 1 head x `block`
 // tokens (128 bytes per row, 128-byte swizzle).
@@ -1234,14 +1391,14 @@ bool make_kv_map(CUtensorMap* map, const void* base, const Shape& s, const int64
   if (!enc) return false;
   const bool paged = s.pages.table != nullptr;
   if (s.kv8) {
-    // e4m3 codes: one box is a whole row of d bytes x 1 head x `block` tokens.  L2
+    // e4m3 codes: one box is a whole row of d bytes x 1 head x a stage's tokens.  L2
     // fills are kept to the row's 128 bytes: with the heads of a token side by side,
     // a wider fill would bring rows that no selected block needs.
     cuuint64_t dims8[4] = {(cuuint64_t)s.d, (cuuint64_t)s.h,
                            (cuuint64_t)(paged ? s.block : s.max_kv),
                            (cuuint64_t)(paged ? s.pages.pages : s.batch)};
     cuuint64_t strides8[3] = {(cuuint64_t)str[2], (cuuint64_t)str[1], (cuuint64_t)str[0]};
-    cuuint32_t box8[4] = {(cuuint32_t)s.d, 1, (cuuint32_t)s.block, 1};
+    cuuint32_t box8[4] = {(cuuint32_t)s.d, 1, (cuuint32_t)q8_unit(s), 1};
     cuuint32_t ones[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims8, strides8,
                box8, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1293,17 +1450,17 @@ struct AttnPlan {
 // Stage count that keeps every block of a stage on the same warps (a warp waits
 // only on the stages of blocks it processes): with fewer 16-token slices per
 // block than consumer warps, a multiple of the warp cycle.
-int stage_count(int want, int nsub, int nc, int most) {
+int stage_count(int want, int nsub, int nc) {
   const int cycle = nsub >= nc ? 1 : nc / nsub;
-  want = max(2, min(most, want));
+  want = max(2, min(8, want));
   return max(cycle, want - want % cycle);
 }
 
 AttnPlan plan_attn(const Shape& s) {
   AttnPlan pl;
   const bool kv8 = s.kv8;
-  pl.stage_bytes = (kv8 ? 2u : 4u) * s.d * s.block;  // K and V tiles of one block
-  const int most = kv8 ? 32 : 8;                     // stages
+  // K and V tiles: of one block, or one stage's share of it
+  pl.stage_bytes = kv8 ? 2u * s.d * q8_unit(s) : 4u * s.d * s.block;
   const int nsub = s.block / 16;
   const int64_t rows_g = (int64_t)s.batch * s.n_q * s.h;
   pl.total = rows_g * s.topk;
@@ -1328,14 +1485,15 @@ AttnPlan plan_attn(const Shape& s) {
     const size_t fixed = 1024 + merge_r + 4 * (3 * (size_t)pl.list_cap + 1);
     const size_t cap = (size_t)max_smem_optin();
     const int fit = cap > fixed ? (int)((cap - fixed) / (pl.stage_bytes + 16)) : 0;
-    pl.stages = stage_count(fit, nsub, kStreamNC, most);  // fit >= 3 for every supported shape
+    // bf16: fit >= 3 for every supported shape
+    pl.stages = kv8 ? min(32, fit) : stage_count(fit, nsub, kStreamNC);
     pl.region_bytes = pl.stages * pl.stage_bytes + merge_r;
     pl.merge_off = pl.stages * pl.stage_bytes;
   } else {
     // Two CTAs per SM when the stages allow it, else one with deeper buffering.
     int want = (int)((100u * 1024u) / pl.stage_bytes);
     if (want < 2) want = min(4, (int)((200u * 1024u) / pl.stage_bytes));
-    pl.stages = stage_count(want, nsub, 4, 8);
+    pl.stages = kv8 ? max(4, min(8, want)) : stage_count(want, nsub, 4);
     pl.region_bytes = max(pl.stages * pl.stage_bytes, merge_bytes);
     pl.merge_off = 0;
     pl.ctas = (int)rows_g;
@@ -1345,6 +1503,21 @@ AttnPlan plan_attn(const Shape& s) {
   }
   pl.smem_bytes = 1024 + pl.region_bytes + 16 * pl.stages + 4 * (3 * (size_t)pl.list_cap + 1);
   return pl;
+}
+
+// Calls f with a warp state for the shape's head dim, group size and block: 64 tokens
+// at a time, or the block when it is smaller; groups of more than 8 heads hold twice
+// as many scores and outputs per thread and take 32.
+template <class F>
+cudaError_t with_q8_state(const Shape& s, F f) {
+  auto pick = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (s.G <= 8)
+      return s.block >= 64 ? f(WarpStateTQ<D, 4>()) : s.block == 32 ? f(WarpStateTQ<D, 2>())
+                                                                    : f(WarpStateTQ<D, 1>());
+    return s.block >= 32 ? f(WarpStateQ<D, 2>()) : f(WarpStateQ<D, 1>());
+  };
+  return s.d == 128 ? pick(std::integral_constant<int, 128>()) : pick(std::integral_constant<int, 64>());
 }
 
 }  // namespace
@@ -1432,6 +1605,7 @@ cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const void* k,
   a.pg = s.pages;
   a.ks = s.ks;
   a.vs = s.vs;
+  a.unit = q8_unit(s);
   cudaError_t err;
   if (!pl.stream && !s.kv8 && kv_attn_supported(s)) {
     CUtensorMap tmq;
@@ -1448,13 +1622,9 @@ cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const void* k,
   };
   if (!pl.stream) {
     constexpr int NT = 5 * 32;
-    if (kv8) {
-      if (s.d == 128)
-        return s.G <= 8 ? launch(sparse_attn_rows_kernel<128, WarpStateTQ<128>>, NT)
-                        : launch(sparse_attn_rows_kernel<128, WarpStateQ<128>>, NT);
-      return s.G <= 8 ? launch(sparse_attn_rows_kernel<64, WarpStateTQ<64>>, NT)
-                      : launch(sparse_attn_rows_kernel<64, WarpStateQ<64>>, NT);
-    }
+    if (kv8)
+      return with_q8_state(
+          s, [&](auto ws) { return launch(sparse_attn_rows_kernel<decltype(ws)::kD, decltype(ws)>, NT); });
     return s.d == 128 ? launch(sparse_attn_rows_kernel<128, WarpState<128>>, NT)
                       : launch(sparse_attn_rows_kernel<64, WarpState<64>>, NT);
   }
@@ -1472,13 +1642,11 @@ cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const void* k,
   }
   constexpr int NT = (kStreamNC + 1) * 32;
   // groups of up to 8 heads take the swapped MMA operands
-  if (kv8) {
-    if (s.d == 128)
-      return s.G <= 8 ? launch(sparse_attn_stream_kernel<128, kStreamNC, WarpStateTQ<128>>, NT)
-                      : launch(sparse_attn_stream_kernel<128, kStreamNC, WarpStateQ<128>>, NT);
-    return s.G <= 8 ? launch(sparse_attn_stream_kernel<64, kStreamNC, WarpStateTQ<64>>, NT)
-                    : launch(sparse_attn_stream_kernel<64, kStreamNC, WarpStateQ<64>>, NT);
-  }
+  if (kv8)
+    return with_q8_state(s, [&](auto ws) {
+      using WS = decltype(ws);
+      return launch(sparse_attn_stream_kernel<WS::kD, kStreamNC, WS>, NT);
+    });
   if (s.d == 128)
     return s.G <= 8 ? launch(sparse_attn_stream_kernel<128, kStreamNC, WarpStateT<128>>, NT)
                     : launch(sparse_attn_stream_kernel<128, kStreamNC, WarpState<128>>, NT);
