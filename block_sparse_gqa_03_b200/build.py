@@ -18,8 +18,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmsa.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["msa_api.cu", "index_scores.cu", "index_scores_tc.cu", "topk.cu", "sparse_attn.cu",
-           "sparse_attn_kv.cu", "append_kv.cu", "shard.cu", "kv_q8.cu", "index_scores_q8.cu"]
-HEADERS = ["common.cuh", "kernels.h", "q8.cuh", "sm100.cuh"]
+           "sparse_attn_kv.cu", "append_kv.cu", "shard.cu", "kv_q8.cu", "index_scores_q8.cu",
+           "sparse_attn_q8.cu"]
+HEADERS = ["attn_common.cuh", "common.cuh", "kernels.h", "q8.cuh", "sm100.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
