@@ -192,6 +192,11 @@ struct AttnPlan {
 
 // 8-bit cache (sparse_attn_q8.cu).
 AttnPlan plan_attn_q8(const Shape& s);
+// K or V codes as a 4-D tensor [batch][token][kv head][dim], or for a paged cache
+// [page][token in page][kv head][dim]; one box is `dims` codes x 1 head x `tokens`,
+// swizzled by its row size when `swizzle`.
+bool make_codes_map(CUtensorMap* map, const void* base, const Shape& s, const int64_t* str,
+                    int dims, int tokens, bool swizzle);
 cudaError_t run_attn_q8(const Shape& s, const AttnPlan& pl, const void* k, const void* v,
                         const AttnArgs& a, cudaStream_t stream);
 

@@ -843,7 +843,7 @@ bool make_rows_map(CUtensorMap* map, uint16_t* base, int64_t rows, int d) {
 
 size_t attn_partial_bytes(const Shape& s) {
   const AttnPlan pl = plan_attn(s);
-  if (!pl.stream) return !s.kv8 && kv_attn_supported(s) ? kv_workspace_bytes(s) : 0;
+  if (!pl.stream) return kv_attn_supported(s) ? kv_workspace_bytes(s) : 0;
   const size_t n = (size_t)s.batch * s.n_q * s.H * pl.smax;
   const size_t rows_g = (size_t)s.batch * s.n_q * s.h;
   return n * (size_t)(s.d + 1) * sizeof(float) + rows_g * sizeof(int) + 512;
@@ -851,7 +851,7 @@ size_t attn_partial_bytes(const Shape& s) {
 
 int attn_launches(const Shape& s) {
   const AttnPlan pl = plan_attn(s);
-  return !pl.stream && !s.kv8 && kv_attn_supported(s) ? kv_launches(s) : 1;
+  return !pl.stream && kv_attn_supported(s) ? kv_launches(s) : 1;
 }
 
 int* attn_merge_counters(const Shape& s, void* partials, int* count) {
@@ -871,10 +871,18 @@ cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const void* k,
                                cudaStream_t stream, bool counters_zeroed, int* fixed_counters) {
   const AttnPlan pl = plan_attn(s);
   if (pl.smem_bytes > kSmemCap) return cudaErrorInvalidValue;
+  // gathered by block on tcgen05 (prefill), else streamed or one CTA per row
+  const bool by_block = !pl.stream && kv_attn_supported(s);
   CUtensorMap tmk, tmv;
-  if (!s.kv8 && (!make_kv_map(&tmk, static_cast<const uint16_t*>(k), s, s.k_s) ||
-                 !make_kv_map(&tmv, static_cast<const uint16_t*>(v), s, s.v_s)))
-    return cudaErrorInvalidValue;
+  if (!s.kv8) {
+    if (!make_kv_map(&tmk, static_cast<const uint16_t*>(k), s, s.k_s) ||
+        !make_kv_map(&tmv, static_cast<const uint16_t*>(v), s, s.v_s))
+      return cudaErrorInvalidValue;
+  } else if (by_block) {
+    if (!make_codes_map(&tmk, k, s, s.k_s, 64, s.block, false) ||
+        !make_codes_map(&tmv, v, s, s.v_s, 64, s.block, false))
+      return cudaErrorInvalidValue;
+  }
   AttnArgs a;
   a.q = q;
   a.q_s0 = s.q_s[0];
@@ -915,13 +923,13 @@ cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const void* k,
   a.vs = s.vs;
   a.unit = s.block;
   cudaError_t err;
-  if (!pl.stream && s.kv8) return run_attn_q8(s, pl, k, v, a, stream);
-  if (!pl.stream && kv_attn_supported(s)) {
+  if (by_block) {
     CUtensorMap tmq;
     if (!make_q_group_map(&tmq, q, s)) return cudaErrorInvalidValue;
     return launch_kv_attn(s, tmq, tmk, tmv, q, ids, out, lse, partials, partial_bytes, st, stream);
   }
   if (!pl.stream) {
+    if (s.kv8) return run_attn_q8(s, pl, k, v, a, stream);
     const dim3 grid((unsigned)pl.ctas);
     if (s.d == 128) {
       err = cudaFuncSetAttribute(sparse_attn_rows_kernel<128>,

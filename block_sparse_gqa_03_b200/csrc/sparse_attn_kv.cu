@@ -35,10 +35,19 @@
 //                 row, each owning one P region in tensor memory;
 //   warps 12-15   output warpgroup: O / l from tensor memory to the partials
 //                 (staged per warp in shared memory, written by TMA stores).
+// 8-bit cache (template parameter Q8): K and V arrive as e4m3 codes and are widened in
+// shared memory, K to bf16 (the queries' type) and V to f16, in which P is written too
+// (11 bits instead of 8 at no cost).  The codes of a block land in the upper half of
+// the place of their widened form, and one warp widens them from the bottom up, so that
+// it never overwrites codes it has not read: no shared memory is needed for them.
+// Warp 0 does nothing else there (it walks the blocks, one ahead of the tiles), and
+// warps 2 and 3 gather Q.  A block's K scale joins the softmax scale of the tile and its
+// V scale the 1 / l of the output.
 // Buffers: 2-4 Q tiles (released when S is computed), 2 K/V stages, and in tensor
 // memory 3-4 slots, each holding a tile's S and then its O, plus the two P
 // regions.  Every wait is bounded.
 #include "kernels.h"
+#include "q8.cuh"
 #include "sm100.cuh"
 
 namespace msa {
@@ -88,6 +97,7 @@ struct KvArgs {
   DeviceStatus* st;
   uint64_t wait_ns;
   KvPages pg;  // table == nullptr: contiguous K/V
+  const float *ks, *vs;  // 8-bit cache: scales per (block, KV head)
 };
 
 __device__ __forceinline__ int visible_from_length(const KvArgs& a, int L, int t) {
@@ -279,7 +289,56 @@ struct KvSmem {
   static_assert(BYTES <= LIMIT, "shared memory");
 };
 
-template <int D, int BLK>
+// Widens N bytes of codes that lie in the upper half of the 2 N bytes at `dst` (rows of
+// 64 codes, one 64-dim atom after the other) into 16-bit rows in the 128-byte swizzle,
+// bf16 or f16.  One warp; 16 codes per lane and step.  A step reads 512 bytes and then
+// writes 1024, its last byte never beyond the next step's codes.  Rows [r0, BLK) of each
+// atom become zeros.
+template <int BLK, uint32_t N, bool F16>
+__device__ __forceinline__ void widen_codes(uint32_t dst, int r0, int lane) {
+  const int row = lane >> 2, c = lane & 3;
+#pragma unroll 2
+  for (uint32_t g = 0; g < N / 512; ++g) {
+    uint32_t x[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(dst + N + g * 512 + lane * 16)
+                 : "memory");
+    if ((int)((g * 8) % BLK) + row >= r0) x[0] = x[1] = x[2] = x[3] = 0u;
+    __syncwarp();
+    const uint32_t out = dst + g * 1024;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t lo = q8::lo_f16x2(x[2 * h + e]), hi = q8::hi_f16x2(x[2 * h + e]);
+        if constexpr (F16) {
+          y[2 * e] = lo;
+          y[2 * e + 1] = hi;
+        } else {
+          const float2 a = q8::f16x2_floats(lo), b = q8::f16x2_floats(hi);
+          y[2 * e] = pack_bf16(a.x, a.y);
+          y[2 * e + 1] = pack_bf16(b.x, b.y);
+        }
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + swz128(row, 2 * c + h)),
+                   "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                   : "memory");
+    }
+  }
+}
+
+// Scales of a list's block; a page outside the pool reads as zeros.
+__device__ __forceinline__ void list_scales(const KvArgs& a, int b, int g, int beta, float& ks,
+                                            float& vs) {
+  int64_t plane = (int64_t)b * a.nblk + beta;
+  if (a.pg.table != nullptr) plane = kv_page(a.pg, b, beta, a.st);
+  ks = plane < 0 ? 1.f : __ldg(a.ks + plane * a.h + g);
+  vs = plane < 0 ? 1.f : __ldg(a.vs + plane * a.h + g);
+}
+
+template <int D, int BLK, bool Q8>
 __global__ void __launch_bounds__(kKvThreads, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
@@ -289,6 +348,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   using SM = KvSmem<D, BLK>;
   constexpr int NH = D / 64;
   constexpr int NQ = SM::NQ;
+  constexpr int NG = Q8 ? 2 : 3;            // warps gathering Q
+  constexpr int TQ = (2 * kRows / NG + 31) / 32;  // their loads per lane (NH * 128 / G at most)
   constexpr uint32_t QB = SM::Q, HALF = SM::HALF, KV_BYTES = SM::KV;
   // Tensor memory: NS slots of W columns, each holding a tile's S and then its
   // O (O = P V overwrites the S it was computed from), and two P regions of
@@ -343,7 +404,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       mbar_init(b_sfree + 8 * i, 4);
     }
     for (int i = 0; i < NQ; ++i) {
-      mbar_init(b_qfull + 8 * i, 3);
+      mbar_init(b_qfull + 8 * i, NG);
       mbar_init(b_qempty + 8 * i, 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(b_lfull + 8 * i, 4);
@@ -362,7 +423,53 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   // code under each limit is exactly that branch.
   const int wg = warp >> 2;
   Walker w;
-  if (warp == kWarpProd || warp == kWarpGather || warp == kWarpGather + 1) {
+  if (Q8 && warp == kWarpProd) {
+    // ------------------------------------------------- K/V codes, load and widen
+    tc::regs_dec<kRegsLoad>();
+    if (n > 0) {
+      w.seek(a, tile0);
+      if (lane == 0) {
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+      }
+      constexpr uint32_t RAW = NH * HALF / 2;  // codes of K (or V)
+      int use = 0;
+      for (int tile = tile0;; ++use) {
+        const int s = use & 1;
+        if (use >= 2 &&
+            !mbar_wait_warp(b_kvempty + 8 * s, ((use >> 1) - 1) & 1, a.st, 0x201u, a.wait_ns))
+          break;
+        const uint32_t kd = skv + s * KV_BYTES, vd = kd + NH * HALF;
+        if (lane == 0) {
+          int tok, plane;
+          kv_block_coords(a.pg, w.b, w.beta, BLK, a.st, tok, plane);
+          const uint32_t bar = b_kvland + 8 * s;
+          mbar_arrive_expect_tx(bar, 2 * RAW);
+#pragma unroll
+          for (int hh = 0; hh < NH; ++hh) {
+            tma_load_4d(kd + RAW + hh * (HALF / 2), &tmk, bar, hh * 64, w.g, tok, plane);
+            tma_load_4d(vd + RAW + hh * (HALF / 2), &tmv, bar, hh * 64, w.g, tok, plane);
+          }
+        }
+        __syncwarp();
+        // V rows past the sequence end may hold anything: zeros, so that a zero
+        // probability never meets a non-finite value
+        const int rows = kv_length(a.seq_lens, w.b, a.max_kv, a.st) - w.beta * BLK;
+        if (!mbar_wait_warp(b_kvland + 8 * s, (use >> 1) & 1, a.st, 0x202u, a.wait_ns)) break;
+        widen_codes<BLK, RAW, false>(kd, BLK, lane);
+        widen_codes<BLK, RAW, true>(vd, rows, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_kvfull + 8 * s);
+        tile = w.t1;
+        if (tile >= tile0 + n) break;
+        w.advance(a, tile);
+      }
+      // drain: the last two stages are released once their products complete
+      for (int u = max(0, use - 1); u <= use; ++u)
+        mbar_wait_warp(b_kvempty + 8 * (u & 1), (u >> 1) & 1, a.st, 0x203u, a.wait_ns);
+    }
+  } else if (warp == kWarpProd || warp == kWarpGather || warp == kWarpGather + 1) {
     // ------------------------------------------ K/V producer (warp 0), Q gather
     // Warp 0 loads a block's K/V when the tile walk reaches a new block.  The Q
     // gather: one TMA load per (query, 64-dim atom) brings the query's G heads,
@@ -372,8 +479,8 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     // A tile's query positions are read while the previous tile is issued.
     tc::regs_dec<kRegsLoad>();
     if (n > 0) {
-      const bool kv_role = warp == kWarpProd;
-      const int gi = kv_role ? 0 : warp - kWarpGather + 1;  // gather share
+      const bool kv_role = !Q8 && warp == kWarpProd;
+      const int gi = warp == kWarpProd ? 0 : warp - kWarpGather + NG - 2;  // gather share
       w.seek(a, tile0);
       if (lane == 0) {
         prefetch_tensormap(&tmq);
@@ -383,17 +490,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         }
       }
       const uint32_t rows_bytes = (uint32_t)a.G * 128u;
-      // loads o = gi + 3 (lane + 32 k) of a tile: query o / NH, atom o % NH
-      auto load_t = [&](int first, int nq, int (&tq)[3]) {
+      // loads o = gi + NG (lane + 32 k) of a tile: query o / NH, atom o % NH
+      auto load_t = [&](int first, int nq, int (&tq)[TQ]) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int o = gi + 3 * (lane + 32 * k);
+        for (int k = 0; k < TQ; ++k) {
+          const int o = gi + NG * (lane + 32 * k);
           tq[k] = o < NH * nq ? __ldg(&a.entries[first + o / NH].y) : 0;
         }
       };
       int nq = w.count(a, tile0), qg = w.g, qbb = w.b;
       bool new_block = true;
-      int tq[3];
+      int tq[TQ];
       load_t(w.first(a, tile0), nq, tq);
       int use = -1;
       uint32_t land_par = 0;  // bit s: parity of the next wait on kv_land[s]
@@ -446,14 +553,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (idx >= NQ && q_ok)
           q_ok = mbar_wait_warp(b_qempty + 8 * qb, ((idx / NQ) - 1) & 1, a.st, 0x20au, a.wait_ns);
         const int total = NH * nq;
-        const int mine = q_ok ? (total - gi + 2) / 3 : 0;
+        const int mine = q_ok ? (total - gi + NG - 1) / NG : 0;
         const uint32_t bar = b_qfull + 8 * qb;
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)mine * rows_bytes);
         __syncwarp();
         if (q_ok) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const int o = gi + 3 * (lane + 32 * k);
+          for (int k = 0; k < TQ; ++k) {
+            const int o = gi + NG * (lane + 32 * k);
             if (o < total) {
               const int qi = o / NH, hh = o % NH;
               tma_load_4d(sq + qb * QB + hh * (kRows * 128u) + qi * rows_bytes, &tmq, bar, hh * 64,
@@ -489,7 +596,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         // by more than NS tiles) hold its K/V stage and whether it is the last
         // tile of its block.  No progress for wait_ns records a timeout.
         const uint32_t id_qk = tc::idesc_bf16(kRows, BLK, false);
-        const uint32_t id_pv = tc::idesc_bf16(kRows, D, true);
+        const uint32_t id_pv = Q8 ? tc::idesc_f16(kRows, D, true) : tc::idesc_bf16(kRows, D, true);
         // Shared-memory descriptors of the first Q tile, the first K stage and the
         // first V stage; an operand elsewhere is the base plus its byte offset / 16
         // (the start-address field never carries: shared addresses are < 2^18).
@@ -581,8 +688,19 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       // with block 128 the look-ahead measured 4% slower (more spills) and the
       // position is loaded at the top of the tile's turn.
       constexpr int LA = BLK == 64 ? 2 : 0;
+      float sl_n = a.scale_log2, vs_n = 1.f;  // softmax scale and V scale of the tile
+      if constexpr (Q8) {
+        float ks;
+        list_scales(a, w.b, w.g, w.beta, ks, vs_n);
+        sl_n = a.scale_log2 * ks;
+      }
       auto row_visible = [&](int tile, int& t_row, int& beta_row, int& b_row) {
-        w.advance(a, tile);
+        const bool moved = w.advance(a, tile);
+        if (Q8 && moved) {
+          float ks;
+          list_scales(a, w.b, w.g, w.beta, ks, vs_n);
+          sl_n = a.scale_log2 * ks;
+        }
         t_row = -1;
         if (qi < w.count(a, tile)) t_row = __ldg(&a.entries[w.first(a, tile) + qi].y);
         beta_row = w.beta;
@@ -593,6 +711,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       for (int idx = sw; idx < n; idx += 2) {
         if (LA == 0) row_visible(tile0 + idx, t_n, beta_n, b_n);
         const int t_row = t_n, beta_row = beta_n, b_row = b_n;
+        const float sl = Q8 ? sl_n : a.scale_log2, vs = Q8 ? vs_n : 1.f;
         if (LA > 0 && idx + LA < n) row_visible(tile0 + idx + LA, t_n, beta_n, b_n);
         int vis = BLK;
         if (t_row >= 0) {
@@ -621,7 +740,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           m4[2] = fmax3(m4[2], v[e + 4], v[e + 5]);
           m4[3] = fmax3(m4[3], v[e + 6], v[e + 7]);
         }
-        const float ms = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * a.scale_log2;
+        const float ms = fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl;
         const float msafe = ms != ninf ? ms : 0.f;
         // probabilities (masked keys hold -inf and give exactly 0), their sum and
         // the bf16 P row, written to this warpgroup's P region once the O = P V of
@@ -636,19 +755,18 @@ __global__ void __launch_bounds__(kKvThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float x0, x1;
-            fma2(x0, x1, v[c * 32 + 2 * e], v[c * 32 + 2 * e + 1], a.scale_log2, a.scale_log2,
-                 -msafe, -msafe);
+            fma2(x0, x1, v[c * 32 + 2 * e], v[c * 32 + 2 * e + 1], sl, sl, -msafe, -msafe);
             const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
             const int h2 = 2 * (e & 1);  // two packed pairs of partial sums
             add2(l4[h2], l4[h2 + 1], l4[h2], l4[h2 + 1], p0, p1);
-            pk[e] = pack_bf16(p0, p1);
+            pk[e] = Q8 ? q8::pack_f16(p0, p1) : pack_bf16(p0, p1);
           }
           tc::tmem_st16(pr + c * 16, pk);
         }
         tc::tmem_wait_st();
         const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
         rstat[(idx & 3) * kRows + row] =
-            make_float2(l > 0.f ? 1.f / l : 0.f, (ms != ninf && l > 0.f) ? (msafe + log2f(l)) * kLn2 : ninf);
+            make_float2(l > 0.f ? (Q8 ? vs / l : 1.f / l) : 0.f, (ms != ninf && l > 0.f) ? (msafe + log2f(l)) * kLn2 : ninf);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
@@ -1037,7 +1155,7 @@ KvPlan plan_kv(const Shape& s) {
   return p;
 }
 
-template <int D, int BLK>
+template <int D, int BLK, bool Q8>
 cudaError_t run_kv(const Shape& s, KvArgs& a, const KvPlan& p, const CUtensorMap& tmq,
                    const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmo,
                    uint8_t* ws, cudaStream_t stream) {
@@ -1045,10 +1163,10 @@ cudaError_t run_kv(const Shape& s, KvArgs& a, const KvPlan& p, const CUtensorMap
   // The register reallocation inside the kernel is sized for a launch with
   // kRegsLaunch registers per thread; any other build would wait forever.
   cudaFuncAttributes fa;
-  cudaError_t err = cudaFuncGetAttributes(&fa, kv_attn_kernel<D, BLK>);
+  cudaError_t err = cudaFuncGetAttributes(&fa, kv_attn_kernel<D, BLK, Q8>);
   if (err != cudaSuccess) return err;
   if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
-  err = cudaFuncSetAttribute(kv_attn_kernel<D, BLK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  err = cudaFuncSetAttribute(kv_attn_kernel<D, BLK, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem);
   if (err != cudaSuccess) return err;
   const int sms = num_sms();
@@ -1065,7 +1183,7 @@ cudaError_t run_kv(const Shape& s, KvArgs& a, const KvPlan& p, const CUtensorMap
         (err = launch_pdl(kv_scan_kernel, dim3(1), dim3(1024), 0, stream, a)) != cudaSuccess ||
         (err = launch_pdl(kv_scatter_kernel, dim3(grid), dim3(256), 0, stream, a, BLK)) !=
             cudaSuccess ||
-        (err = launch_pdl(kv_attn_kernel<D, BLK>, dim3(sms), dim3(kKvThreads), smem, stream, tmq,
+        (err = launch_pdl(kv_attn_kernel<D, BLK, Q8>, dim3(sms), dim3(kKvThreads), smem, stream, tmq,
                           tmk, tmv, tmo, a)) != cudaSuccess)
       return err;
     // The combine is launched plainly: as a programmatic dependent of kv_attn
@@ -1136,10 +1254,17 @@ cudaError_t launch_kv_attn(const Shape& s, const CUtensorMap& tmq, const CUtenso
   a.pg = s.pages;
   CUtensorMap tmo;
   if (!make_rows_map(&tmo, a.part_o, p.max_tiles * kRows, s.d)) return cudaErrorInvalidValue;
-  if (s.d == 128 && s.block == 128) return run_kv<128, 128>(s, a, p, tmq, tmk, tmv, tmo, w, stream);
-  if (s.d == 128 && s.block == 64) return run_kv<128, 64>(s, a, p, tmq, tmk, tmv, tmo, w, stream);
-  if (s.d == 64 && s.block == 128) return run_kv<64, 128>(s, a, p, tmq, tmk, tmv, tmo, w, stream);
-  if (s.d == 64 && s.block == 64) return run_kv<64, 64>(s, a, p, tmq, tmk, tmv, tmo, w, stream);
+  a.ks = s.ks;
+  a.vs = s.vs;
+#define MSA_KV_CASE(D_, B_)                                                          \
+  if (s.d == D_ && s.block == B_)                                                    \
+    return s.kv8 ? run_kv<D_, B_, true>(s, a, p, tmq, tmk, tmv, tmo, w, stream)      \
+                 : run_kv<D_, B_, false>(s, a, p, tmq, tmk, tmv, tmo, w, stream);
+  MSA_KV_CASE(128, 128)
+  MSA_KV_CASE(128, 64)
+  MSA_KV_CASE(64, 128)
+  MSA_KV_CASE(64, 64)
+#undef MSA_KV_CASE
   return cudaErrorInvalidValue;
 }
 

@@ -813,27 +813,6 @@ __global__ void __launch_bounds__((NC + 2) * 32, 1)
 // Tokens per stage: 16 KB at most, so that there are more stages than consumer warps.
 int stage_tokens(const Shape& s) { return s.block < 64 ? s.block : 64; }
 
-// K or V codes as a 4-D tensor [batch][token][kv head][dim], or for a paged cache
-// [page][token in page][kv head][dim]; one box is a whole row of d bytes x 1 head x a
-// stage's tokens.  L2 fills are kept to the row's 128 bytes: with the heads of a token
-// side by side, a wider fill would bring rows that no selected block needs.
-bool make_codes_map(CUtensorMap* map, const void* base, const Shape& s, const int64_t* str) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const bool paged = s.pages.table != nullptr;
-  cuuint64_t dims[4] = {(cuuint64_t)s.d, (cuuint64_t)s.h,
-                        (cuuint64_t)(paged ? s.block : s.max_kv),
-                        (cuuint64_t)(paged ? s.pages.pages : s.batch)};
-  cuuint64_t strides[3] = {(cuuint64_t)str[2], (cuuint64_t)str[1], (cuuint64_t)str[0]};
-  cuuint32_t box[4] = {(cuuint32_t)s.d, 1, (cuuint32_t)stage_tokens(s), 1};
-  cuuint32_t ones[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
-             ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             s.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
-
 constexpr int kStreamNC = 6;    // consumer warps of the streaming kernel
 constexpr int kMaxList = 4096;  // entries a streaming CTA compacts up front
 
@@ -855,6 +834,27 @@ cudaError_t with_state(const Shape& s, F f) {
 }
 
 }  // namespace
+
+// L2 fills are kept to 128 bytes, one row of a head: with the heads of a token side by
+// side, a wider fill would bring rows that no selected block needs.
+bool make_codes_map(CUtensorMap* map, const void* base, const Shape& s, const int64_t* str,
+                    int dims, int tokens, bool swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const bool paged = s.pages.table != nullptr;
+  cuuint64_t size[4] = {(cuuint64_t)s.d, (cuuint64_t)s.h,
+                        (cuuint64_t)(paged ? s.block : s.max_kv),
+                        (cuuint64_t)(paged ? s.pages.pages : s.batch)};
+  cuuint64_t strides[3] = {(cuuint64_t)str[2], (cuuint64_t)str[1], (cuuint64_t)str[0]};
+  cuuint32_t box[4] = {(cuuint32_t)dims, 1, (cuuint32_t)tokens, 1};
+  cuuint32_t ones[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle sw = !swizzle      ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                : dims == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                              : CU_TENSOR_MAP_SWIZZLE_64B;
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), size, strides, box,
+             ones, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 AttnPlan plan_attn_q8(const Shape& s) {
   AttnPlan pl;
@@ -897,7 +897,8 @@ AttnPlan plan_attn_q8(const Shape& s) {
 cudaError_t run_attn_q8(const Shape& s, const AttnPlan& pl, const void* k, const void* v,
                         const AttnArgs& args, cudaStream_t stream) {
   CUtensorMap tmk, tmv;
-  if (!make_codes_map(&tmk, k, s, s.k_s) || !make_codes_map(&tmv, v, s, s.v_s))
+  if (!make_codes_map(&tmk, k, s, s.k_s, s.d, stage_tokens(s), true) ||
+      !make_codes_map(&tmv, v, s, s.v_s, s.d, stage_tokens(s), true))
     return cudaErrorInvalidValue;
   AttnArgs a = args;
   a.unit = stage_tokens(s);
