@@ -47,7 +47,7 @@ constexpr uint32_t kTmemCols = 512;
 struct TcArgs {
   int batch, n_q, max_kv, h, block, nblk, causal;
   const int32_t* seq_lens;
-  int n_mtiles, n_gpairs, stages;
+  int n_mtiles, n_gpairs, n_split, stages;
   float* scores;
   int fill_tail;
   DeviceStatus* st;
@@ -111,6 +111,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int x = blockIdx.x;
+  const int sp = x % a.n_split;  // share of the key tiles
+  x /= a.n_split;
   const int mt = a.n_mtiles - 1 - (x % a.n_mtiles);  // late (long) query tiles first
   x /= a.n_mtiles;
   const int gp = x % a.n_gpairs;
@@ -121,7 +123,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int t_last = min(t0 + kQT, a.n_q) - 1;
   const int p_last = L - a.n_q + t_last;
   const int lim_last = max(0, a.causal ? min(L, p_last + 1) : L);
-  const int n_kt = (lim_last + kKT - 1) / kKT;  // key tiles holding a visible key
+  const int n_all = (lim_last + kKT - 1) / kKT;  // key tiles holding a visible key
+  // this CTA's: [kt0, kt0 + n_kt), numbered from 0 below
+  const int kt0 = (int)((int64_t)n_all * sp / a.n_split);
+  const int n_kt = (int)((int64_t)n_all * (sp + 1) / a.n_split) - kt0;
 
   if (threadIdx.x == 0) {
     mbar_init(b_qfull, 1);
@@ -168,13 +173,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int at = 0; at < NATOM; ++at)
             tma_load_3d(k_base + s * K_BYTES + at * ATOM, &tmk, b_kfull + 8 * s, at * 64,
-                        kt * kKT, b);
+                        (kt0 + kt) * kKT, b);
         } else {
           // one box per page of BLK tokens; blocks past the sequence end are not
           // looked up and read as zeros (their keys are masked anyway)
           const int nb_b = (L + BLK - 1) / BLK;
           for (int pi = 0; pi < kKT / BLK; ++pi) {
-            const int beta = kt * (kKT / BLK) + pi;
+            const int beta = (kt0 + kt) * (kKT / BLK) + pi;
             const int64_t page = beta < nb_b ? kv_page(a.pg, b, beta, a.st) : -1;
             const int plane = page < 0 ? (int)a.pg.pages : (int)page;
 #pragma unroll
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int buf = kt & 1;
       if (!mbar_wait_warp(b_afull + 8 * buf, (kt >> 1) & 1, a.st, 0x106u, a.wait_ns)) break;
       tc::fence_after_sync();
-      const int j0 = kt * kKT;
+      const int j0 = (kt0 + kt) * kKT;
       const int vis = lim - j0;  // columns [0, vis) of this tile are visible keys
       float v[kKT];
 #pragma unroll
@@ -325,8 +330,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-    if (srow != nullptr && a.fill_tail && row_ok && ng < ng_valid)
-      for (int beta = n_kt * bpt; beta < a.nblk; ++beta) srow[beta] = ninf;
+    if (srow != nullptr && a.fill_tail && row_ok && ng < ng_valid && sp == a.n_split - 1)
+      for (int beta = n_all * bpt; beta < a.nblk; ++beta) srow[beta] = ninf;
     if constexpr (TOPK) {
       if (row_ok && ng < ng_valid) {
         // the kept ids (empty entries are 0xffff and sort last) and the forced own
@@ -396,7 +401,14 @@ cudaError_t run_tc(const Shape& s, const uint16_t* q_idx, const uint16_t* k_idx,
   cudaError_t err = cudaFuncSetAttribute(index_score_tc_kernel<DI, BLK, TOPK>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  const unsigned grid = (unsigned)((int64_t)s.batch * a.n_gpairs * a.n_mtiles);
+  // Few query tiles (a chunk of a prompt, a short batch): the key tiles are split over
+  // CTAs up to one wave, at least 8 tiles each (every block's score depends on its own
+  // tile alone; the streaming top-k needs them all in one CTA).  2048 queries, 4 groups
+  // of 64 dims, 32K keys: 32 CTAs took 181 us, 4 shares each SPLITUS us.
+  const int64_t ctas = (int64_t)s.batch * a.n_gpairs * a.n_mtiles;
+  const int tiles = (s.max_kv + kKT - 1) / kKT;
+  a.n_split = TOPK ? 1 : (int)max((int64_t)1, min(num_sms() / ctas, (int64_t)tiles / 8));
+  const unsigned grid = (unsigned)(ctas * a.n_split);
   return launch_pdl(index_score_tc_kernel<DI, BLK, TOPK>, dim3(grid), dim3(kTcThreads), smem,
                     stream, tmq, tmk, a);
 }

@@ -657,29 +657,32 @@ class _Q8Call:
                             self.table[0], self.table[1], self.pages)
 
     def run(self, what, op, params, workspace, *args):
-        lib = load_library()
-        need = lib.msa_workspace_size(params, op)
-        if need == 0:  # bad parameters: the call itself says which
-            need = STATUS_BYTES
-        if workspace is None:
-            workspace = self.default_workspace()
-        buf = workspace.buf
+        lib = _lib or load_library()
+        need = lib.msa_workspace_size(params, op) or STATUS_BYTES  # 0: the call says why
         capturing = torch._C._cuda_isCurrentStreamCapturing()
-        if buf is None or buf.numel() < need:
+        if workspace is None and capturing:
+            # a graph gets its own, from its pool: no two graphs share one
+            buf = torch.empty(need, dtype=torch.uint8, device=self.dev)
+            _check(lib.msa_workspace_init(buf.data_ptr(), need, self.stream), "msa_workspace_init")
+        else:
+            if workspace is None:
+                workspace = self.default_workspace()
+            buf = workspace.buf
+            if buf is None or buf.numel() < need:
+                if capturing:
+                    raise RuntimeError("the workspace cannot grow while a graph is captured: run "
+                                       "the call once before, or leave the workspace out")
+                with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, self.dev)):
+                    buf = workspace.get(need)
             if capturing:
-                raise RuntimeError("the workspace cannot grow while a graph is captured: run the "
-                                   "call once before, or pass a Workspace that is large enough")
-            with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, self.dev)):
-                buf = workspace.get(need)
-        if capturing:
-            workspace.hold()
+                workspace.hold()
         rc = getattr(lib, what)(params, *args, buf.data_ptr(), buf.numel(), self.stream)
         if rc != MSA_OK:
             raise MsaError(rc, what)
 
     def default_workspace(self):
         """The device's workspace, one for each stream other than the default one."""
-        key = self.dev.index if self.stream == 0 else (self.dev.index, self.stream)
+        key = (self.dev.index, self.stream) if self.stream else self.dev.index
         if key not in _default_ws:
             _default_ws[key] = Workspace(self.dev)
         return _default_ws[key]

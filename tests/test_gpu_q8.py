@@ -535,7 +535,7 @@ def test_side_stream_and_captured_step():
                                   topk=topk, return_ids=True, return_lse=True, **kw)
 
     ws1, ws2 = msa.Workspace(DEV), msa.Workspace(DEV)
-    with pytest.raises(RuntimeError, match="cannot grow"):
+    with pytest.raises(RuntimeError, match="cannot grow"):  # a workspace of the caller
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             step(c1, *static, msa.Workspace(DEV))
     side = torch.cuda.Stream()
