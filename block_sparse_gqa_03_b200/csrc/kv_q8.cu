@@ -13,10 +13,16 @@
 // count.  One CTA per (sequence, touched block, K head | V head | index key): it
 // holds the block's new rows in registers between the maximum and the rounding, so
 // each new element is read once, and no other CTA touches the scale it replaces.
+// Bound: HBM, 3 bytes per element.  2 x 32K rows of 4 heads of 128 dims (213 MB): 35.3
+// us with CTAs of 128 threads, 40.1 us of 256 (fewer CTAs per SM cover the wait for the
+// maximum); 32.6 us at the measured copy rate.
 //
 // Read (read_kv_q8_kernel).  out = bf16(code * s), exact for power-of-two scales.
 // One CTA per 32 (or block, when smaller) tokens of a sequence: one page lookup and
-// one set of scales serve all its rows.
+// one set of scales serve all its rows.  Bound: HBM writes, 2 of the 3 bytes per
+// element.  The rows above (213 MB, 142 of them written): 43 us, and the same within 3%
+// for pieces of 8 codes, other orders of heads and rows and other CTA sizes; half of
+// the measured copy rate, which is what a copy writes, gives 43 us for the 142 MB.
 #include "kernels.h"
 #include "q8.cuh"
 
@@ -38,7 +44,7 @@ struct Q8Args {
   int group;        // read: tokens per CTA
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // The K head, V head or index key that CTA unit `u` of a token row stands for.
 struct Unit {
@@ -209,23 +215,35 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
     const int cpr = d / 16, shift = __ffs(cpr) - 1;
     const int per_head = rows << shift;
     const int total = heads * per_head;
-    for (int p = threadIdx.x; p < total; p += kThreads) {
-      const int g = p / per_head, rem = p - g * per_head;
-      const int r = rem >> shift, c = rem & (cpr - 1);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      float s = 1.f;
-      if (!bad) {
-        x = ld_stream_u4(codes + plane * st[0] + (row0 + r) * st[1] + (heads > 1 ? g * st[2] : 0) +
-                         c * 16);
-        s = __ldg(scales + scale_at * heads + g);
+    constexpr int U = 4;  // pieces per thread whose loads are under way together
+    for (int p0 = threadIdx.x; p0 < total; p0 += U * kThreads) {
+      uint4 x[U];
+      float s[U];
+      uint16_t* o[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int p = min(p0 + i * kThreads, total - 1);
+        const int g = p / per_head, rem = p - g * per_head;
+        const int r = rem >> shift, c = rem & (cpr - 1);
+        x[i] = make_uint4(0, 0, 0, 0);
+        s[i] = 1.f;
+        if (!bad) {
+          x[i] = ld_stream_u4(codes + plane * st[0] + (row0 + r) * st[1] +
+                              (heads > 1 ? g * st[2] : 0) + c * 16);
+          s[i] = __ldg(scales + scale_at * heads + g);
+        }
+        o[i] = out + ((out0 + r) * heads + g) * d + c * 16;
       }
-      uint16_t* o = out + ((out0 + r) * heads + g) * d + c * 16;
-      *reinterpret_cast<uint4*>(o) =
-          make_uint4(value2(q8::lo_f16x2(x.x), s), value2(q8::hi_f16x2(x.x), s),
-                     value2(q8::lo_f16x2(x.y), s), value2(q8::hi_f16x2(x.y), s));
-      *reinterpret_cast<uint4*>(o + 8) =
-          make_uint4(value2(q8::lo_f16x2(x.z), s), value2(q8::hi_f16x2(x.z), s),
-                     value2(q8::lo_f16x2(x.w), s), value2(q8::hi_f16x2(x.w), s));
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (p0 + i * kThreads >= total) break;
+        *reinterpret_cast<uint4*>(o[i]) =
+            make_uint4(value2(q8::lo_f16x2(x[i].x), s[i]), value2(q8::hi_f16x2(x[i].x), s[i]),
+                       value2(q8::lo_f16x2(x[i].y), s[i]), value2(q8::hi_f16x2(x[i].y), s[i]));
+        *reinterpret_cast<uint4*>(o[i] + 8) =
+            make_uint4(value2(q8::lo_f16x2(x[i].z), s[i]), value2(q8::hi_f16x2(x[i].z), s[i]),
+                       value2(q8::lo_f16x2(x[i].w), s[i]), value2(q8::hi_f16x2(x[i].w), s[i]));
+      }
     }
   };
   plane_of(a.k, a.k_s, a.ks, a.h, a.d, a.k_out);
@@ -281,7 +299,8 @@ cudaError_t launch_append_kv_q8(const Shape& s, const uint16_t* k_new, const uin
   };
   if (pieces <= 1) return run(append_kv_q8_kernel<1>);
   if (pieces <= 2) return run(append_kv_q8_kernel<2>);
-  return run(append_kv_q8_kernel<4>);  // block 128, 128 dims: 1024 pieces
+  if (pieces <= 4) return run(append_kv_q8_kernel<4>);
+  return run(append_kv_q8_kernel<8>);  // block 128, 128 dims: 1024 pieces
 }
 
 cudaError_t launch_read_kv_q8(const Shape& s, const Q8Cache& c, int64_t base, int64_t n,

@@ -867,8 +867,10 @@ AttnPlan plan_attn_q8(const Shape& s) {
   pl.stream = rows_g < 4LL * num_sms();
   if (pl.stream) {
     pl.ctas = num_sms();
-    pl.per = (int)((pl.total + pl.ctas - 1) / pl.ctas);
-    if (pl.per > kMaxList) pl.per = kMaxList;
+    // an even share, but a block for each consumer warp: in a small problem, finer shares
+    // only add partials to merge
+    pl.per = max((int)((pl.total + pl.ctas - 1) / pl.ctas), min(kStreamNC, s.topk));
+    pl.per = min(pl.per, kMaxList);
     pl.ctas = (int)((pl.total + pl.per - 1) / pl.per);
     pl.smax = (s.topk - 1) / pl.per + 2;
     pl.list_cap = pl.per;

@@ -13,7 +13,6 @@ present, these functions raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import struct
 import threading
@@ -582,140 +581,121 @@ def q8_cache(*, h, d, d_idx, block, batch=None, max_kv=None, num_pages=None, dev
                    codes(planes, rows, d_idx), ones(*scales, h), ones(*scales, h), ones(*scales))
 
 
-# msa_params_t as one packed record: a decode step makes several calls of a few
-# microseconds each, and filling the ctypes structure field by field takes longer
-# than some of the kernels.
+# msa_params_t as one packed record.  A decode step makes several calls of a few
+# microseconds each, so the marshalling below is kept short: filling the ctypes
+# structure field by field takes longer than some of the kernels.
 _PARAMS = struct.Struct("11ifP17qP2q")
 assert _PARAMS.size == ctypes.sizeof(Params)
-_NO3 = (0, 0, 0)
 _F8 = (torch.float8_e4m3fn, torch.uint8)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
-def _q8_codes(name, t, planes, rows, tail, dev):
+def _codes(name, t, shape, dev):
     """Checks a code tensor and returns its outer strides."""
-    if t.dtype not in _F8:
-        raise ValueError("%s must hold e4m3 codes (float8_e4m3fn or uint8)" % name)
-    if t.device != dev or t.shape[0] != planes or t.shape[1] != rows or t.shape[2:] != tail:
-        raise ValueError("%s has shape %s on %s" % (name, tuple(t.shape), t.device))
+    if t.shape != shape or t.dtype not in _F8 or t.get_device() != dev:
+        raise ValueError("%s must hold e4m3 codes (float8_e4m3fn or uint8) of shape %s on device %d"
+                         % (name, tuple(shape), dev))
     st = t.stride()
     if st[-1] != 1:
         raise ValueError("innermost axis of %s must be contiguous" % name)
     return st[:-1]
 
 
-def _q8_scale(name, t, shape, dev):
-    if t.dtype != torch.float32 or t.device != dev or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a dense fp32 tensor of shape %s on %s" % (name, shape, dev))
-
-
-def _q8_dense(name, t, shape, dtype, dev):
-    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a dense %s tensor of shape %s on %s"
+def _dense(name, t, shape, dtype, dev):
+    """Checks a dense tensor and returns its address."""
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous()):
+        raise ValueError("%s must be a dense %s tensor of shape %s on device %d"
                          % (name, dtype, tuple(shape), dev))
+    return t.data_ptr()
 
 
-class _Q8Call:
-    """One call's cache geometry, stream and workspace."""
-
-    def __init__(self, dev, batch, codes, block, seq_lens, block_table, max_kv, stream):
-        if dev.type != "cuda":
-            raise ValueError("the 8-bit cache calls need CUDA tensors")
-        self.dev = dev
-        self.block = block
-        self.planes = codes.shape[0]
-        self.paged = block_table is not None
-        if self.paged:
-            if max_kv is None:
-                raise ValueError("a paged KV cache needs max_kv")
-            self.max_kv, self.rows, self.pages = int(max_kv), block, self.planes
-            if (block_table.dtype != torch.int32 or block_table.dim() != 2
-                    or block_table.device != dev or block_table.shape[0] != batch
-                    or block_table.stride(1) != 1 or block_table.shape[1] * block < self.max_kv):
-                raise ValueError("block_table must be int32 [batch, >= ceil(max_kv / block)]")
-            self.table = (block_table.data_ptr(), block_table.stride(0) if batch > 1
-                          else max(block_table.stride(0), block_table.shape[1]))
-        else:
-            if self.planes != batch:
-                raise ValueError("the cache holds %d sequences, not %d" % (self.planes, batch))
-            self.max_kv = self.rows = codes.shape[1]
-            if max_kv is not None and int(max_kv) != self.max_kv:
-                raise ValueError("max_kv is the cache's token axis, %d" % self.max_kv)
-            self.pages, self.table = 0, (0, 0)
-        self.nblk = -(-self.max_kv // block)
-        self.scales = (self.planes,) if self.paged else (batch, self.nblk)
-        self.lens = 0
-        if seq_lens is not None:
-            _q8_dense("seq_lens", seq_lens, (batch,), torch.int32, dev)
-            self.lens = seq_lens.data_ptr()
-        self.stream = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
-                       else stream.cuda_stream)
-
-    def params(self, batch, n_q, H, h, d, d_idx, topk, causal=True, force=False, scale=0.0,
-               q=_NO3, k=_NO3, v=_NO3, qi=_NO3, ki=(0, 0), o=_NO3):
-        return _PARAMS.pack(batch, n_q, self.max_kv, H, h, d, d_idx, self.block, topk,
-                            bool(causal), bool(force), scale, self.lens, *q, *k, *v, *qi, *ki, *o,
-                            self.table[0], self.table[1], self.pages)
-
-    def run(self, what, op, params, workspace, *args):
-        lib = _lib or load_library()
-        need = lib.msa_workspace_size(params, op) or STATUS_BYTES  # 0: the call says why
-        capturing = torch._C._cuda_isCurrentStreamCapturing()
-        if workspace is None and capturing:
-            # a graph gets its own, from its pool: no two graphs share one
-            buf = torch.empty(need, dtype=torch.uint8, device=self.dev)
-            _check(lib.msa_workspace_init(buf.data_ptr(), need, self.stream), "msa_workspace_init")
-        else:
-            if workspace is None:
-                workspace = self.default_workspace()
-            buf = workspace.buf
-            if buf is None or buf.numel() < need:
-                if capturing:
-                    raise RuntimeError("the workspace cannot grow while a graph is captured: run "
-                                       "the call once before, or leave the workspace out")
-                with torch.cuda.stream(torch.cuda.ExternalStream(self.stream, self.dev)):
-                    buf = workspace.get(need)
-            if capturing:
-                workspace.hold()
-        rc = getattr(lib, what)(params, *args, buf.data_ptr(), buf.numel(), self.stream)
-        if rc != MSA_OK:
-            raise MsaError(rc, what)
-
-    def default_workspace(self):
-        """The device's workspace, one for each stream other than the default one."""
-        key = (self.dev.index, self.stream) if self.stream else self.dev.index
-        if key not in _default_ws:
-            _default_ws[key] = Workspace(self.dev)
-        return _default_ws[key]
+def _rows(name, t, shape, dev):
+    """Checks a bf16 tensor of rows and returns its outer strides."""
+    st = t.stride()
+    if t.shape != shape or t.dtype is not _BF16 or t.get_device() != dev or st[-1] != 1:
+        raise ValueError("%s must be bf16 of shape %s on device %d, its innermost axis contiguous"
+                         % (name, tuple(shape), dev))
+    return st[:-1]
 
 
-def _on_device(f):
-    """Runs a call with its tensors' device current."""
+def _made(like, name, t, shape, dtype, dev, wanted=True):
+    """An output: the one given, checked, or a new one (on `like`'s device); its address."""
+    if t is None:
+        if not wanted:
+            return None, None
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _dense(name, t, shape, dtype, dev)
 
-    @functools.wraps(f)
-    def call(first, *args, **kw):
-        dev = first.device
-        if dev.type != "cuda" or dev.index == torch.cuda.current_device():
-            return f(first, *args, **kw)
+
+def _cache_geometry(codes, batch, block, seq_lens, block_table, max_kv):
+    """(device, planes, rows, max_kv, nblk, leading shape of the scales, (seq_lens,),
+    (block_table, table_stride, num_pages)) of a contiguous or paged cache."""
+    dev = codes.get_device()
+    if dev < 0:
+        raise ValueError("the 8-bit cache calls need CUDA tensors")
+    planes, rows = codes.shape[:2]
+    lens = 0 if seq_lens is None else _dense("seq_lens", seq_lens, (batch,), _I32, dev)
+    if block_table is None:
+        if planes != batch:
+            raise ValueError("the cache holds %d sequences, not %d" % (planes, batch))
+        if max_kv is not None and max_kv != rows:
+            raise ValueError("max_kv is the cache's token axis, %d" % rows)
+        nblk = -(-rows // block)
+        return dev, planes, rows, rows, nblk, (planes, nblk), lens, (0, 0, 0)
+    if max_kv is None:
+        raise ValueError("a paged KV cache needs max_kv")
+    nblk = -(-max_kv // block)
+    b, width = block_table.shape
+    st = block_table.stride()
+    if (block_table.dtype is not _I32 or block_table.get_device() != dev or b != batch
+            or width < nblk or st[1] != 1):
+        raise ValueError("block_table must be int32 [batch, >= ceil(max_kv / block)]")
+    table = (block_table.data_ptr(), st[0] if b > 1 else width, planes)
+    return dev, planes, block, max_kv, nblk, (planes,), lens, table
+
+
+def _run_q8(what, op, params, dev, workspace, stream, args, need=None):
+    """One library call; ``need``: workspace bytes, when they do not depend on the shape."""
+    lib = _lib or load_library()
+    if _get_device() != dev:
         with torch.cuda.device(dev):
-            return f(first, *args, **kw)
+            return _run_q8(what, op, params, dev, workspace, stream, args, need)
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if need is None:
+        need = lib.msa_workspace_size(params, op) or STATUS_BYTES  # 0: the call says why
+    if workspace is None and _capturing():
+        # a graph gets its own, from its pool: no two graphs share one
+        buf = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib.msa_workspace_init(buf.data_ptr(), need, raw), "msa_workspace_init")
+    else:
+        if workspace is None:
+            # the device's workspace, one for each stream other than the default one
+            key = (dev, raw) if raw else dev
+            workspace = _default_ws.get(key)
+            if workspace is None:
+                workspace = _default_ws[key] = Workspace(torch.device("cuda", dev))
+            capturing = False
+        else:
+            capturing = _capturing()
+        buf = workspace.buf
+        if buf is None or buf.numel() < need:
+            if capturing:
+                raise RuntimeError("the workspace cannot grow while a graph is captured: run the "
+                                   "call once before, or leave the workspace out")
+            with torch.cuda.stream(torch.cuda.ExternalStream(raw, dev)):
+                buf = workspace.get(need)
+        if capturing:
+            workspace.hold()
+    rc = getattr(lib, what)(params, *args, buf.data_ptr(), buf.numel(), raw)
+    if rc != MSA_OK:
+        raise MsaError(rc, what)
 
-    return call
 
-
-def _need(x, what):
-    if x is None:
-        raise ValueError("%s is missing" % what)
-    return x
-
-
-def _bf16_outer(name, t, dev):
-    """Strides of a bf16 tensor's outer axes."""
-    if t.dtype != torch.bfloat16 or t.device != dev or t.stride(-1) != 1:
-        raise ValueError("%s must be bf16 on %s, its innermost axis contiguous" % (name, dev))
-    return t.stride()[:-1]
-
-
-@_on_device
 def msa_append_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new=None, v_new=None,
                      k_idx_new=None, *, block, seq_lens=None, block_table=None, max_kv=None,
                      workspace: Workspace | None = None, stream=None):
@@ -723,139 +703,133 @@ def msa_append_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new=None, v_n
     k_idx_new [b, n_new, d_idx] (dense) are quantised into positions L_b - n_new + t, and
     the scales of the blocks they fall into are set (see ``include/msa.h``).  Any of the
     new tensors may be None (its part of the cache is not written)."""
-    ref = next((t for t in (k_new, v_new, k_idx_new) if t is not None), None)
+    ref = k_new if k_new is not None else v_new if v_new is not None else k_idx_new
     if ref is None:
         raise ValueError("no new rows")
-    b, n, h, d = ref.shape[0], ref.shape[1], k.shape[2], k.shape[3]
+    b, n = ref.shape[:2]
+    dev, planes, rows, cap, _, lead, lens, table = _cache_geometry(k, b, block, seq_lens,
+                                                                   block_table, max_kv)
+    h, d = k.shape[2:]
     d_idx = k_idx.shape[-1]
-    c = _Q8Call(k.device, b, k, block, seq_lens, block_table, max_kv, stream)
-    ks, vs, kis = _q8_strides(c, k, v, k_idx, k_scale, v_scale, k_idx_scale, h, d, d_idx)
-    for name, t, tail in (("k_new", k_new, (h, d)), ("v_new", v_new, (h, d)),
-                          ("k_idx_new", k_idx_new, (d_idx,))):
-        if t is not None:
-            _q8_dense(name, t, (b, n) + tail, torch.bfloat16, c.dev)
-    p = c.params(b, n, h, h, d, d_idx, 1, k=ks, v=vs, ki=kis)
-    c.run("msa_append_kv_q8", MSA_OP_APPEND_KV_Q8, p, workspace, _ptr(k_new), _ptr(v_new),
-          _ptr(k_idx_new), k.data_ptr(), v.data_ptr(), k_idx.data_ptr(), k_scale.data_ptr(),
-          v_scale.data_ptr(), k_idx_scale.data_ptr())
+    shape, new_shape = (planes, rows, h, d), (b, n, h, d)
+    params = _PARAMS.pack(
+        b, n, cap, h, h, d, d_idx, block, 1, 1, 0, 0.0, lens, 0, 0, 0,
+        *_codes("k", k, shape, dev), *_codes("v", v, shape, dev), 0, 0, 0,
+        *_codes("k_idx", k_idx, (planes, rows, d_idx), dev), 0, 0, 0, *table)
+    args = (None if k_new is None else _dense("k_new", k_new, new_shape, _BF16, dev),
+            None if v_new is None else _dense("v_new", v_new, new_shape, _BF16, dev),
+            None if k_idx_new is None else _dense("k_idx_new", k_idx_new, (b, n, d_idx), _BF16, dev),
+            k.data_ptr(), v.data_ptr(), k_idx.data_ptr(),
+            _dense("k_scale", k_scale, lead + (h,), _F32, dev),
+            _dense("v_scale", v_scale, lead + (h,), _F32, dev),
+            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev))
+    _run_q8("msa_append_kv_q8", MSA_OP_APPEND_KV_Q8, params, dev, workspace, stream, args,
+            STATUS_BYTES)
 
 
-def _q8_strides(c, k, v, k_idx, k_scale, v_scale, k_idx_scale, h, d, d_idx):
-    ks = _q8_codes("k", k, c.planes, c.rows, (h, d), c.dev)
-    vs = _q8_codes("v", v, c.planes, c.rows, (h, d), c.dev)
-    kis = _q8_codes("k_idx", k_idx, c.planes, c.rows, (d_idx,), c.dev)
-    _q8_scale("k_scale", k_scale, c.scales + (h,), c.dev)
-    _q8_scale("v_scale", v_scale, c.scales + (h,), c.dev)
-    _q8_scale("k_idx_scale", k_idx_scale, c.scales, c.dev)
-    return ks, vs, kis
-
-
-@_on_device
 def msa_read_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, *, n, token_base=0, block,
                    seq_lens=None, block_table=None, max_kv=None, k_out=None, v_out=None,
                    k_idx_out=None, workspace: Workspace | None = None, stream=None):
     """Rows [token_base, token_base + n) of every sequence of an 8-bit cache as bf16:
     (k [b, n, h, d], v, k_idx [b, n, d_idx]).  Rows at positions past a sequence's end are
     left as they were in the given outputs, and are zeros in those made here."""
-    h, d, d_idx = k.shape[2], k.shape[3], k_idx.shape[-1]
-    b = block_table.shape[0] if block_table is not None else k.shape[0]
-    c = _Q8Call(k.device, b, k, block, seq_lens, block_table, max_kv, stream)
-    ks, vs, kis = _q8_strides(c, k, v, k_idx, k_scale, v_scale, k_idx_scale, h, d, d_idx)
-    outs = []
-    for name, t, tail in (("k_out", k_out, (h, d)), ("v_out", v_out, (h, d)),
-                          ("k_idx_out", k_idx_out, (d_idx,))):
-        if t is None:
-            t = torch.zeros((b, n) + tail, dtype=torch.bfloat16, device=c.dev)
-        else:
-            _q8_dense(name, t, (b, n) + tail, torch.bfloat16, c.dev)
-        outs.append(t)
-    p = c.params(b, n, h, h, d, d_idx, 1, k=ks, v=vs, ki=kis)
-    c.run("msa_read_kv_q8", MSA_OP_READ_KV_Q8, p, workspace, k.data_ptr(), v.data_ptr(),
-          k_idx.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_idx_scale.data_ptr(),
-          int(token_base), *(t.data_ptr() for t in outs))
-    return tuple(outs)
+    b = k.shape[0] if block_table is None else block_table.shape[0]
+    dev, planes, rows, cap, _, lead, lens, table = _cache_geometry(k, b, block, seq_lens,
+                                                                   block_table, max_kv)
+    h, d = k.shape[2:]
+    d_idx = k_idx.shape[-1]
+    shape, out_shape, idx_shape = (planes, rows, h, d), (b, n, h, d), (b, n, d_idx)
+    params = _PARAMS.pack(
+        b, n, cap, h, h, d, d_idx, block, 1, 1, 0, 0.0, lens, 0, 0, 0,
+        *_codes("k", k, shape, dev), *_codes("v", v, shape, dev), 0, 0, 0,
+        *_codes("k_idx", k_idx, (planes, rows, d_idx), dev), 0, 0, 0, *table)
+    if k_out is None:
+        k_out = torch.zeros(out_shape, dtype=_BF16, device=dev)
+    if v_out is None:
+        v_out = torch.zeros(out_shape, dtype=_BF16, device=dev)
+    if k_idx_out is None:
+        k_idx_out = torch.zeros(idx_shape, dtype=_BF16, device=dev)
+    args = (k.data_ptr(), v.data_ptr(), k_idx.data_ptr(),
+            _dense("k_scale", k_scale, lead + (h,), _F32, dev),
+            _dense("v_scale", v_scale, lead + (h,), _F32, dev),
+            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev), int(token_base),
+            _dense("k_out", k_out, out_shape, _BF16, dev),
+            _dense("v_out", v_out, out_shape, _BF16, dev),
+            _dense("k_idx_out", k_idx_out, idx_shape, _BF16, dev))
+    _run_q8("msa_read_kv_q8", MSA_OP_READ_KV_Q8, params, dev, workspace, stream, args,
+            STATUS_BYTES)
+    return k_out, v_out, k_idx_out
 
 
-def _q8_index(q_idx, k_idx, k_idx_scale, block, topk, causal, force_own_block, seq_lens,
-              block_table, max_kv, stream):
-    b, n_q, h, d_idx = q_idx.shape
-    c = _Q8Call(q_idx.device, b, k_idx, block, seq_lens, block_table, max_kv, stream)
-    kis = _q8_codes("k_idx", k_idx, c.planes, c.rows, (d_idx,), c.dev)
-    _q8_scale("k_idx_scale", k_idx_scale, c.scales, c.dev)
-    p = c.params(b, n_q, h, h, 64, d_idx, topk, causal, force_own_block,
-                 qi=_bf16_outer("q_idx", q_idx, c.dev), ki=kis)
-    return c, p
-
-
-def _q8_out(t, name, shape, dtype, dev, wanted=True):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev) if wanted else None
-    _q8_dense(name, t, shape, dtype, dev)
-    return t
-
-
-@_on_device
 def msa_block_scores_q8(q_idx, k_idx, k_idx_scale, *, block, causal=True, seq_lens=None,
                         block_scores=None, block_table=None, max_kv=None,
                         workspace: Workspace | None = None, stream=None):
     """msa_block_scores over the 8-bit index key: fp32 [b, n_q, h, nblk]."""
-    c, p = _q8_index(q_idx, k_idx, k_idx_scale, block, 1, causal, False, seq_lens, block_table,
-                     max_kv, stream)
-    block_scores = _q8_out(block_scores, "block_scores", q_idx.shape[:3] + (c.nblk,),
-                           torch.float32, c.dev)
-    c.run("msa_block_scores_q8", MSA_OP_BLOCK_SCORES_Q8, p, workspace, q_idx.data_ptr(),
-          k_idx.data_ptr(), k_idx_scale.data_ptr(), block_scores.data_ptr())
+    shape = b, n, h, d_idx = q_idx.shape
+    dev, planes, rows, cap, nblk, lead, lens, table = _cache_geometry(
+        k_idx, b, block, seq_lens, block_table, max_kv)
+    block_scores, scores = _made(q_idx, "block_scores", block_scores, (b, n, h, nblk), _F32,
+                                 dev)
+    params = _PARAMS.pack(
+        b, n, cap, h, h, 64, d_idx, block, 1, bool(causal), 0, 0.0, lens, 0, 0, 0, 0, 0, 0, 0, 0, 0,
+        *_rows("q_idx", q_idx, shape, dev), *_codes("k_idx", k_idx, (planes, rows, d_idx), dev),
+        0, 0, 0, *table)
+    args = (q_idx.data_ptr(), k_idx.data_ptr(),
+            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev), scores)
+    _run_q8("msa_block_scores_q8", MSA_OP_BLOCK_SCORES_Q8, params, dev, workspace, stream, args,
+            STATUS_BYTES if n == 1 else None)
     return block_scores
 
 
-@_on_device
 def msa_index_select_q8(q_idx, k_idx, k_idx_scale, *, block, topk, causal=True,
                         force_own_block=False, seq_lens=None, return_scores=False,
                         block_ids=None, block_scores=None, block_table=None, max_kv=None,
                         workspace: Workspace | None = None, stream=None):
     """msa_index_select over the 8-bit index key: block ids int32 [b, n_q, h, topk] (and the
     fp32 block scores if asked)."""
-    c, p = _q8_index(q_idx, k_idx, k_idx_scale, block, topk, causal, force_own_block, seq_lens,
-                     block_table, max_kv, stream)
-    lead = q_idx.shape[:3]
-    block_ids = _q8_out(block_ids, "block_ids", lead + (topk,), torch.int32, c.dev)
-    block_scores = _q8_out(block_scores, "block_scores", lead + (c.nblk,), torch.float32, c.dev,
-                           return_scores)
-    c.run("msa_index_select_q8", MSA_OP_INDEX_SELECT_Q8, p, workspace, q_idx.data_ptr(),
-          k_idx.data_ptr(), k_idx_scale.data_ptr(), block_ids.data_ptr(), _ptr(block_scores))
+    shape = b, n, h, d_idx = q_idx.shape
+    dev, planes, rows, cap, nblk, lead, lens, table = _cache_geometry(
+        k_idx, b, block, seq_lens, block_table, max_kv)
+    block_ids, ids = _made(q_idx, "block_ids", block_ids, (b, n, h, topk), _I32, dev)
+    block_scores, scores = _made(q_idx, "block_scores", block_scores, (b, n, h, nblk), _F32, dev,
+                                 return_scores)
+    params = _PARAMS.pack(
+        b, n, cap, h, h, 64, d_idx, block, topk, bool(causal), bool(force_own_block), 0.0, lens,
+        0, 0, 0, 0, 0, 0, 0, 0, 0, *_rows("q_idx", q_idx, shape, dev),
+        *_codes("k_idx", k_idx, (planes, rows, d_idx), dev), 0, 0, 0, *table)
+    args = (q_idx.data_ptr(), k_idx.data_ptr(),
+            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev), ids, scores)
+    _run_q8("msa_index_select_q8", MSA_OP_INDEX_SELECT_Q8, params, dev, workspace, stream, args)
     return (block_ids, block_scores) if return_scores else block_ids
 
 
-@_on_device
 def msa_sparse_attn_q8(q, k, v, k_scale, v_scale, block_ids, *, block, causal=True,
                        seq_lens=None, softmax_scale=0.0, return_lse=False, out=None, lse=None,
                        block_table=None, max_kv=None, workspace: Workspace | None = None,
                        stream=None):
     """msa_sparse_attn over the 8-bit cache: bf16 output [b, n_q, H, d] (and fp32 lse
     [b, n_q, H] if asked)."""
-    b, n_q, H, d = q.shape
+    shape = b, n, H, d = q.shape
+    dev, planes, rows, cap, _, lead, lens, table = _cache_geometry(k, b, block, seq_lens,
+                                                                   block_table, max_kv)
     h = k.shape[2]
-    c = _Q8Call(q.device, b, k, block, seq_lens, block_table, max_kv, stream)
-    ks = _q8_codes("k", k, c.planes, c.rows, (h, d), c.dev)
-    vs = _q8_codes("v", v, c.planes, c.rows, (h, d), c.dev)
-    _q8_scale("k_scale", k_scale, c.scales + (h,), c.dev)
-    _q8_scale("v_scale", v_scale, c.scales + (h,), c.dev)
     topk = block_ids.shape[-1]
-    _q8_dense("block_ids", block_ids, (b, n_q, h, topk), torch.int32, c.dev)
     if out is None:
-        out = torch.empty((b, n_q, H, d), dtype=torch.bfloat16, device=c.dev)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the queries' shape")
-    lse = _q8_out(lse, "lse", (b, n_q, H), torch.float32, c.dev, return_lse)
-    p = c.params(b, n_q, H, h, d, 32, topk, causal, scale=softmax_scale,
-                 q=_bf16_outer("q", q, c.dev), k=ks, v=vs, o=_bf16_outer("out", out, c.dev))
-    c.run("msa_sparse_attn_q8", MSA_OP_SPARSE_ATTN_Q8, p, workspace, q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_ids.data_ptr(),
-          out.data_ptr(), _ptr(lse))
+        out = torch.empty_like(q)
+    lse, lse_ptr = _made(q, "lse", lse, (b, n, H), _F32, dev, return_lse)
+    cshape = (planes, rows, h, d)
+    params = _PARAMS.pack(
+        b, n, cap, H, h, d, 32, block, topk, bool(causal), 0, softmax_scale, lens,
+        *_rows("q", q, shape, dev), *_codes("k", k, cshape, dev), *_codes("v", v, cshape, dev),
+        0, 0, 0, 0, 0, *_rows("out", out, shape, dev), *table)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            _dense("k_scale", k_scale, lead + (h,), _F32, dev),
+            _dense("v_scale", v_scale, lead + (h,), _F32, dev),
+            _dense("block_ids", block_ids, (b, n, h, topk), _I32, dev), out.data_ptr(), lse_ptr)
+    _run_q8("msa_sparse_attn_q8", MSA_OP_SPARSE_ATTN_Q8, params, dev, workspace, stream, args)
     return (out, lse) if return_lse else out
 
 
-@_on_device
 def msa_forward_q8(q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, *, block, topk,
                    causal=True, force_own_block=False, seq_lens=None, softmax_scale=0.0,
                    out=None, block_ids=None, block_scores=None, lse=None, return_ids=False,
@@ -863,28 +837,28 @@ def msa_forward_q8(q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, *, bloc
                    workspace: Workspace | None = None, stream=None):
     """msa_forward over the 8-bit cache; returns out, plus (ids, scores, lse) when asked,
     in that order."""
-    b, n_q, H, d = q.shape
-    h, d_idx = k.shape[2], q_idx.shape[-1]
-    c = _Q8Call(q.device, b, k, block, seq_lens, block_table, max_kv, stream)
-    ks, vs, kis = _q8_strides(c, k, v, k_idx, k_scale, v_scale, k_idx_scale, h, d, d_idx)
-    if q_idx.shape != (b, n_q, h, d_idx):
-        raise ValueError("q_idx must have shape [b, n_q, h, d_idx]")
+    shape = b, n, H, d = q.shape
+    dev, planes, rows, cap, nblk, lead, lens, table = _cache_geometry(k, b, block, seq_lens,
+                                                                      block_table, max_kv)
+    h, d_idx = k.shape[2], k_idx.shape[-1]
     if out is None:
-        out = torch.empty((b, n_q, H, d), dtype=torch.bfloat16, device=c.dev)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the queries' shape")
-    lead = (b, n_q, h)
-    block_ids = _q8_out(block_ids, "block_ids", lead + (topk,), torch.int32, c.dev, return_ids)
-    block_scores = _q8_out(block_scores, "block_scores", lead + (c.nblk,), torch.float32, c.dev,
-                           return_scores)
-    lse = _q8_out(lse, "lse", (b, n_q, H), torch.float32, c.dev, return_lse)
-    p = c.params(b, n_q, H, h, d, d_idx, topk, causal, force_own_block, softmax_scale,
-                 q=_bf16_outer("q", q, c.dev), k=ks, v=vs, qi=_bf16_outer("q_idx", q_idx, c.dev),
-                 ki=kis, o=_bf16_outer("out", out, c.dev))
-    c.run("msa_forward_q8", MSA_OP_FORWARD_Q8, p, workspace, q.data_ptr(), k.data_ptr(),
-          v.data_ptr(), q_idx.data_ptr(), k_idx.data_ptr(), k_scale.data_ptr(),
-          v_scale.data_ptr(), k_idx_scale.data_ptr(), out.data_ptr(), _ptr(block_ids),
-          _ptr(block_scores), _ptr(lse))
+        out = torch.empty_like(q)
+    block_ids, ids = _made(q, "block_ids", block_ids, (b, n, h, topk), _I32, dev, return_ids)
+    block_scores, scores = _made(q, "block_scores", block_scores, (b, n, h, nblk), _F32, dev,
+                                 return_scores)
+    lse, lse_ptr = _made(q, "lse", lse, (b, n, H), _F32, dev, return_lse)
+    cshape = (planes, rows, h, d)
+    params = _PARAMS.pack(
+        b, n, cap, H, h, d, d_idx, block, topk, bool(causal), bool(force_own_block), softmax_scale,
+        lens, *_rows("q", q, shape, dev), *_codes("k", k, cshape, dev),
+        *_codes("v", v, cshape, dev), *_rows("q_idx", q_idx, (b, n, h, d_idx), dev),
+        *_codes("k_idx", k_idx, (planes, rows, d_idx), dev), *_rows("out", out, shape, dev), *table)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_idx.data_ptr(), k_idx.data_ptr(),
+            _dense("k_scale", k_scale, lead + (h,), _F32, dev),
+            _dense("v_scale", v_scale, lead + (h,), _F32, dev),
+            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev), out.data_ptr(), ids, scores,
+            lse_ptr)
+    _run_q8("msa_forward_q8", MSA_OP_FORWARD_Q8, params, dev, workspace, stream, args)
     res = [out]
     if return_ids:
         res.append(block_ids)
