@@ -59,8 +59,6 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
 template <int DI, int NT, int MT>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     index_scan_q8_kernel(const __grid_constant__ CUtensorMap tmk, ScanQ8Args a) {
-  grid_dep_wait();
-  grid_dep_launch();
   constexpr int NW = kWarps;
   constexpr int NC = DI / 16;  // 16-dim steps
   extern __shared__ uint8_t smem_raw[];
@@ -79,6 +77,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     fence_mbar_init();
     if (warp == 0) prefetch_tensormap(&tmk);
   }
+  grid_dep_wait();  // nothing above needs the kernels before this one
+  grid_dep_launch();
   const bool skip = status_failed(a.st);
   // this CTA's share of the items, counted over the sequences' block counts
   int total = 0;

@@ -109,16 +109,17 @@ __device__ __forceinline__ int visible_limit(const KvArgs& a, int b, int t) {
   return visible_from_length(a, kv_length(a.seq_lens, b, a.max_kv, a.st), t);
 }
 
-// Valid slot of the chunk: a block id that exists and holds a visible token.
-__device__ __forceinline__ bool slot_block(const KvArgs& a, int64_t pos, int& b, int& g, int& t,
+// Valid slot of the chunk: a block id that exists and holds a visible token.  Slots of
+// a chunk and rows of a problem fit 32 bits.
+__device__ __forceinline__ bool slot_block(const KvArgs& a, int pos, int& b, int& g, int& t,
                                            int& beta, int BLK) {
-  const int64_t bt_rel = pos / ((int64_t)a.h * a.topk);
-  const int rem = (int)(pos % ((int64_t)a.h * a.topk));
-  g = rem / a.topk;
-  const int64_t bt = a.bt0 + bt_rel;
-  b = (int)(bt / a.n_q);
-  t = (int)(bt % a.n_q);
-  beta = a.ids[(bt * a.h + g) * a.topk + rem % a.topk];
+  const int per_bt = a.h * a.topk;
+  beta = __ldg(a.ids + a.bt0 * per_bt + pos);
+  const int bt_rel = pos / per_bt;
+  g = (pos - bt_rel * per_bt) / a.topk;
+  const int bt = (int)a.bt0 + bt_rel;
+  b = bt / a.n_q;
+  t = bt - b * a.n_q;
   if (beta < 0) return false;
   if (beta >= a.nblk) {
     record_error(a.st, kErrDeviceAssert, (uint32_t)bt);
@@ -131,9 +132,9 @@ __device__ __forceinline__ bool slot_block(const KvArgs& a, int64_t pos, int& b,
 __global__ void kv_count_kernel(KvArgs a, int BLK) {
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t n = (int64_t)a.nbt * a.h * a.topk;
-  for (int64_t pos = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; pos < n;
-       pos += (int64_t)gridDim.x * blockDim.x) {
+  const int n = a.nbt * a.h * a.topk;  // at most 2^30
+  for (int pos = (int)(blockIdx.x * blockDim.x + threadIdx.x); pos < n;
+       pos += (int)(gridDim.x * blockDim.x)) {
     int b, g, t, beta;
     if (slot_block(a, pos, b, g, t, beta, BLK))
       atomicAdd(&a.counts[((int64_t)b * a.h + g) * a.nblk + beta], 1);
@@ -199,19 +200,20 @@ __global__ void __launch_bounds__(1024) kv_scan_kernel(KvArgs a) {
 __global__ void kv_scatter_kernel(KvArgs a, int BLK) {
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t n = (int64_t)a.nbt * a.h * a.topk;
-  for (int64_t pos = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; pos < n;
-       pos += (int64_t)gridDim.x * blockDim.x) {
+  const int n = a.nbt * a.h * a.topk;  // at most 2^30
+  for (int pos = (int)(blockIdx.x * blockDim.x + threadIdx.x); pos < n;
+       pos += (int)(gridDim.x * blockDim.x)) {
     int b, g, t, beta;
     if (slot_block(a, pos, b, g, t, beta, BLK)) {
       const int64_t j = ((int64_t)b * a.h + g) * a.nblk + beta;
       const int k = atomicAdd(&a.counts[j], 1);
-      a.entries[a.offs[j] + k] = make_int2((int)pos, t);
+      a.entries[a.offs[j] + k] = make_int2(pos, t);
       a.slot_row[pos] = (a.toffs[j] + k / a.qpt) * kRows + (k % a.qpt) * a.G;
     } else {
       // no partial for this slot: the merge reads the marks, not the ids
       a.slot_row[pos] = -1;
-      for (int hh = 0; hh < a.G; ++hh) a.part_lse[pos * a.G + hh] = -__int_as_float(0x7f800000);
+      for (int hh = 0; hh < a.G; ++hh)
+        a.part_lse[(int64_t)pos * a.G + hh] = -__int_as_float(0x7f800000);
     }
   }
 }
