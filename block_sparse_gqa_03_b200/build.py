@@ -2,7 +2,8 @@
 
 ``python -m block_sparse_gqa_03_b200.build`` (or ``__graft_entry__.build()``)
 runs nvcc once per source for sm_100a and links a shared library next to this
-file.  The library exports only the C ABI of ``include/msa.h``.
+file.  The library exports only the C ABI of ``include/msa.h``.  The binding's
+marshalling extension ``_marshal.so`` is compiled next to it.
 """
 
 from __future__ import annotations
@@ -16,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmsa.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")  # Python extension: argument checks of the q8 calls
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["msa_api.cu", "index_scores.cu", "index_scores_tc.cu", "topk.cu", "sparse_attn.cu",
            "sparse_attn_kv.cu", "append_kv.cu", "shard.cu", "kv_q8.cu", "index_scores_q8.cu",
@@ -64,7 +66,31 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    build_marshal(force, verbose)
     return LIB
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compiles the marshalling extension against this interpreter's and torch's headers."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "marshal.cpp")
+    if force or _stale(MARSHAL, [src, os.path.join(ROOT, "include", "msa.h")]):
+        inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+        tmp = MARSHAL + ".tmp%d" % os.getpid()
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+               "-fvisibility=hidden", "-I" + inc,
+               "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+               "-I" + sysconfig.get_paths()["include"], src, "-o", tmp, "-L" + lib,
+               "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":

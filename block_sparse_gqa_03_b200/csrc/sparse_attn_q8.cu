@@ -870,6 +870,11 @@ AttnPlan plan_attn_q8(const Shape& s) {
     // an even share, but a block for each consumer warp: in a small problem, finer shares
     // only add partials to merge
     pl.per = max((int)((pl.total + pl.ctas - 1) / pl.ctas), min(kStreamNC, s.topk));
+    // Whole rows where that adds at most a block per warp (2 us): a split row's partials
+    // are published and merged in 3 to 4 us.  (One sequence of 2 groups with 8 blocks:
+    // SMALLA us with split rows, SMALLB us without.)
+    const int whole = (pl.per + s.topk - 1) / s.topk * s.topk;
+    if (whole - pl.per <= kStreamNC) pl.per = whole;
     pl.per = min(pl.per, kMaxList);
     pl.ctas = (int)((pl.total + pl.per - 1) / pl.per);
     pl.smax = (s.topk - 1) / pl.per + 2;

@@ -13,8 +13,8 @@ present, these functions raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 import threading
 from typing import NamedTuple
 
@@ -22,6 +22,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmsa.so")
+MARSHAL_PATH = os.path.join(_HERE, "_marshal.so")
 STATUS_BYTES = 4096  # the workspace's status region (status word, decode merge counters)
 
 MSA_OK = 0
@@ -581,119 +582,74 @@ def q8_cache(*, h, d, d_idx, block, batch=None, max_kv=None, num_pages=None, dev
                    codes(planes, rows, d_idx), ones(*scales, h), ones(*scales, h), ones(*scales))
 
 
-# msa_params_t as one packed record.  A decode step makes several calls of a few
-# microseconds each, so the marshalling below is kept short: filling the ctypes
-# structure field by field takes longer than some of the kernels.
-_PARAMS = struct.Struct("11ifP17qP2q")
-assert _PARAMS.size == ctypes.sizeof(Params)
-_F8 = (torch.float8_e4m3fn, torch.uint8)
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _get_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
-def _codes(name, t, shape, dev):
-    """Checks a code tensor and returns its outer strides."""
-    if t.shape != shape or t.dtype not in _F8 or t.get_device() != dev:
-        raise ValueError("%s must hold e4m3 codes (float8_e4m3fn or uint8) of shape %s on device %d"
-                         % (name, tuple(shape), dev))
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError("innermost axis of %s must be contiguous" % name)
-    return st[:-1]
+def _marshal_module():
+    """The marshalling extension (``csrc/marshal.cpp``), bound to the loaded library."""
+    global _marshal
+    lib = load_library()
+    if not os.path.exists(MARSHAL_PATH):
+        raise RuntimeError("_marshal.so is not built (run __graft_entry__.build() or "
+                           "python -m block_sparse_gqa_03_b200.build)")
+    spec = importlib.util.spec_from_file_location("block_sparse_gqa_03_b200._marshal",
+                                                  MARSHAL_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    names = ("workspace_size", "append_kv_q8", "read_kv_q8", "block_scores_q8",
+             "index_select_q8", "sparse_attn_q8", "forward_q8")
+    module.bind(*(ctypes.cast(getattr(lib, "msa_" + n), ctypes.c_void_p).value for n in names))
+    _marshal = module
+    return module
 
 
-def _dense(name, t, shape, dtype, dev):
-    """Checks a dense tensor and returns its address."""
-    if (t.shape != shape or t.dtype is not dtype or t.get_device() != dev
-            or not t.is_contiguous()):
-        raise ValueError("%s must be a dense %s tensor of shape %s on device %d"
-                         % (name, dtype, tuple(shape), dev))
-    return t.data_ptr()
+_marshal = None
 
 
-def _rows(name, t, shape, dev):
-    """Checks a bf16 tensor of rows and returns its outer strides."""
-    st = t.stride()
-    if t.shape != shape or t.dtype is not _BF16 or t.get_device() != dev or st[-1] != 1:
-        raise ValueError("%s must be bf16 of shape %s on device %d, its innermost axis contiguous"
-                         % (name, tuple(shape), dev))
-    return st[:-1]
-
-
-def _made(like, name, t, shape, dtype, dev, wanted=True):
-    """An output: the one given, checked, or a new one (on `like`'s device); its address."""
-    if t is None:
-        if not wanted:
-            return None, None
-        t = like.new_empty(shape, dtype=dtype)
-        return t, t.data_ptr()
-    return t, _dense(name, t, shape, dtype, dev)
-
-
-def _cache_geometry(codes, batch, block, seq_lens, block_table, max_kv):
-    """(device, planes, rows, max_kv, nblk, leading shape of the scales, (seq_lens,),
-    (block_table, table_stride, num_pages)) of a contiguous or paged cache."""
-    dev = codes.get_device()
+def _run_q8(what, entry, like, workspace, stream, args):
+    """One library call through the marshalling extension, on ``like``'s device.  The
+    extension checks every tensor, and answers with the library's status or, before it
+    launches anything, with minus the workspace bytes it needs."""
+    dev = like.get_device()
     if dev < 0:
         raise ValueError("the 8-bit cache calls need CUDA tensors")
-    planes, rows = codes.shape[:2]
-    lens = 0 if seq_lens is None else _dense("seq_lens", seq_lens, (batch,), _I32, dev)
-    if block_table is None:
-        if planes != batch:
-            raise ValueError("the cache holds %d sequences, not %d" % (planes, batch))
-        if max_kv is not None and max_kv != rows:
-            raise ValueError("max_kv is the cache's token axis, %d" % rows)
-        nblk = -(-rows // block)
-        return dev, planes, rows, rows, nblk, (planes, nblk), lens, (0, 0, 0)
-    if max_kv is None:
-        raise ValueError("a paged KV cache needs max_kv")
-    nblk = -(-max_kv // block)
-    b, width = block_table.shape
-    st = block_table.stride()
-    if (block_table.dtype is not _I32 or block_table.get_device() != dev or b != batch
-            or width < nblk or st[1] != 1):
-        raise ValueError("block_table must be int32 [batch, >= ceil(max_kv / block)]")
-    table = (block_table.data_ptr(), st[0] if b > 1 else width, planes)
-    return dev, planes, block, max_kv, nblk, (planes,), lens, table
-
-
-def _run_q8(what, op, params, dev, workspace, stream, args, need=None):
-    """One library call; ``need``: workspace bytes, when they do not depend on the shape."""
-    lib = _lib or load_library()
     if _get_device() != dev:
         with torch.cuda.device(dev):
-            return _run_q8(what, op, params, dev, workspace, stream, args, need)
+            return _run_q8(what, entry, like, workspace, stream, args)
+    call = getattr(_marshal or _marshal_module(), entry)
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if need is None:
-        need = lib.msa_workspace_size(params, op) or STATUS_BYTES  # 0: the call says why
-    if workspace is None and _capturing():
-        # a graph gets its own, from its pool: no two graphs share one
-        buf = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(lib.msa_workspace_init(buf.data_ptr(), need, raw), "msa_workspace_init")
-    else:
+    capturing = _capturing()
+    if workspace is None and not capturing:
+        # the device's workspace, one for each stream other than the default one
+        key = (dev, raw) if raw else dev
+        workspace = _default_ws.get(key)
         if workspace is None:
-            # the device's workspace, one for each stream other than the default one
-            key = (dev, raw) if raw else dev
-            workspace = _default_ws.get(key)
-            if workspace is None:
-                workspace = _default_ws[key] = Workspace(torch.device("cuda", dev))
-            capturing = False
+            workspace = _default_ws[key] = Workspace(torch.device("cuda", dev))
+    rc = call(*args, None if workspace is None else workspace.buf, raw)
+    if rc < 0:
+        if workspace is None:
+            # a captured graph gets its own, from its pool: no two graphs share one
+            buf = torch.empty(-rc, dtype=torch.uint8, device=like.device)
+            _check(_lib.msa_workspace_init(buf.data_ptr(), -rc, raw), "msa_workspace_init")
+        elif capturing:
+            raise RuntimeError("the workspace cannot grow while a graph is captured: run the "
+                               "call once before, or leave the workspace out")
         else:
-            capturing = _capturing()
-        buf = workspace.buf
-        if buf is None or buf.numel() < need:
-            if capturing:
-                raise RuntimeError("the workspace cannot grow while a graph is captured: run the "
-                                   "call once before, or leave the workspace out")
             with torch.cuda.stream(torch.cuda.ExternalStream(raw, dev)):
-                buf = workspace.get(need)
-        if capturing:
-            workspace.hold()
-    rc = getattr(lib, what)(params, *args, buf.data_ptr(), buf.numel(), raw)
+                buf = workspace.get(-rc)
+        rc = call(*args, buf, raw)
     if rc != MSA_OK:
         raise MsaError(rc, what)
+    if capturing and workspace is not None:
+        workspace.hold()
+
+
+def _blocks(codes, block, block_table, max_kv):
+    """Blocks of a sequence's capacity."""
+    return -(-(codes.shape[1] if block_table is None else max_kv or 0) // block)
 
 
 def msa_append_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new=None, v_new=None,
@@ -703,28 +659,11 @@ def msa_append_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new=None, v_n
     k_idx_new [b, n_new, d_idx] (dense) are quantised into positions L_b - n_new + t, and
     the scales of the blocks they fall into are set (see ``include/msa.h``).  Any of the
     new tensors may be None (its part of the cache is not written)."""
-    ref = k_new if k_new is not None else v_new if v_new is not None else k_idx_new
-    if ref is None:
+    if k_new is None and v_new is None and k_idx_new is None:
         raise ValueError("no new rows")
-    b, n = ref.shape[:2]
-    dev, planes, rows, cap, _, lead, lens, table = _cache_geometry(k, b, block, seq_lens,
-                                                                   block_table, max_kv)
-    h, d = k.shape[2:]
-    d_idx = k_idx.shape[-1]
-    shape, new_shape = (planes, rows, h, d), (b, n, h, d)
-    params = _PARAMS.pack(
-        b, n, cap, h, h, d, d_idx, block, 1, 1, 0, 0.0, lens, 0, 0, 0,
-        *_codes("k", k, shape, dev), *_codes("v", v, shape, dev), 0, 0, 0,
-        *_codes("k_idx", k_idx, (planes, rows, d_idx), dev), 0, 0, 0, *table)
-    args = (None if k_new is None else _dense("k_new", k_new, new_shape, _BF16, dev),
-            None if v_new is None else _dense("v_new", v_new, new_shape, _BF16, dev),
-            None if k_idx_new is None else _dense("k_idx_new", k_idx_new, (b, n, d_idx), _BF16, dev),
-            k.data_ptr(), v.data_ptr(), k_idx.data_ptr(),
-            _dense("k_scale", k_scale, lead + (h,), _F32, dev),
-            _dense("v_scale", v_scale, lead + (h,), _F32, dev),
-            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev))
-    _run_q8("msa_append_kv_q8", MSA_OP_APPEND_KV_Q8, params, dev, workspace, stream, args,
-            STATUS_BYTES)
+    _run_q8("msa_append_kv_q8", "append", k, workspace, stream,
+            (k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new, v_new, k_idx_new, block, seq_lens,
+             block_table, max_kv))
 
 
 def msa_read_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, *, n, token_base=0, block,
@@ -733,31 +672,20 @@ def msa_read_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, *, n, token_base=
     """Rows [token_base, token_base + n) of every sequence of an 8-bit cache as bf16:
     (k [b, n, h, d], v, k_idx [b, n, d_idx]).  Rows at positions past a sequence's end are
     left as they were in the given outputs, and are zeros in those made here."""
-    b = k.shape[0] if block_table is None else block_table.shape[0]
-    dev, planes, rows, cap, _, lead, lens, table = _cache_geometry(k, b, block, seq_lens,
-                                                                   block_table, max_kv)
-    h, d = k.shape[2:]
-    d_idx = k_idx.shape[-1]
-    shape, out_shape, idx_shape = (planes, rows, h, d), (b, n, h, d), (b, n, d_idx)
-    params = _PARAMS.pack(
-        b, n, cap, h, h, d, d_idx, block, 1, 1, 0, 0.0, lens, 0, 0, 0,
-        *_codes("k", k, shape, dev), *_codes("v", v, shape, dev), 0, 0, 0,
-        *_codes("k_idx", k_idx, (planes, rows, d_idx), dev), 0, 0, 0, *table)
-    if k_out is None:
-        k_out = torch.zeros(out_shape, dtype=_BF16, device=dev)
-    if v_out is None:
-        v_out = torch.zeros(out_shape, dtype=_BF16, device=dev)
-    if k_idx_out is None:
-        k_idx_out = torch.zeros(idx_shape, dtype=_BF16, device=dev)
-    args = (k.data_ptr(), v.data_ptr(), k_idx.data_ptr(),
-            _dense("k_scale", k_scale, lead + (h,), _F32, dev),
-            _dense("v_scale", v_scale, lead + (h,), _F32, dev),
-            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev), int(token_base),
-            _dense("k_out", k_out, out_shape, _BF16, dev),
-            _dense("v_out", v_out, out_shape, _BF16, dev),
-            _dense("k_idx_out", k_idx_out, idx_shape, _BF16, dev))
-    _run_q8("msa_read_kv_q8", MSA_OP_READ_KV_Q8, params, dev, workspace, stream, args,
-            STATUS_BYTES)
+    if k_out is None or v_out is None or k_idx_out is None:
+        b = k.shape[0] if block_table is None else block_table.shape[0]
+        shape = (b, n) + tuple(k.shape[2:])
+        if k_out is None:
+            k_out = k.new_zeros(shape, dtype=_BF16)
+        if v_out is None:
+            v_out = k.new_zeros(shape, dtype=_BF16)
+        if k_idx_out is None:
+            k_idx_out = k.new_zeros((b, n, k_idx.shape[-1]), dtype=_BF16)
+    if k_out.shape[1] != n:
+        raise ValueError("k_out holds %d rows, not %d" % (k_out.shape[1], n))
+    _run_q8("msa_read_kv_q8", "read", k, workspace, stream,
+            (k, v, k_idx, k_scale, v_scale, k_idx_scale, k_out, v_out, k_idx_out, token_base,
+             block, seq_lens, block_table, max_kv))
     return k_out, v_out, k_idx_out
 
 
@@ -765,19 +693,12 @@ def msa_block_scores_q8(q_idx, k_idx, k_idx_scale, *, block, causal=True, seq_le
                         block_scores=None, block_table=None, max_kv=None,
                         workspace: Workspace | None = None, stream=None):
     """msa_block_scores over the 8-bit index key: fp32 [b, n_q, h, nblk]."""
-    shape = b, n, h, d_idx = q_idx.shape
-    dev, planes, rows, cap, nblk, lead, lens, table = _cache_geometry(
-        k_idx, b, block, seq_lens, block_table, max_kv)
-    block_scores, scores = _made(q_idx, "block_scores", block_scores, (b, n, h, nblk), _F32,
-                                 dev)
-    params = _PARAMS.pack(
-        b, n, cap, h, h, 64, d_idx, block, 1, bool(causal), 0, 0.0, lens, 0, 0, 0, 0, 0, 0, 0, 0, 0,
-        *_rows("q_idx", q_idx, shape, dev), *_codes("k_idx", k_idx, (planes, rows, d_idx), dev),
-        0, 0, 0, *table)
-    args = (q_idx.data_ptr(), k_idx.data_ptr(),
-            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev), scores)
-    _run_q8("msa_block_scores_q8", MSA_OP_BLOCK_SCORES_Q8, params, dev, workspace, stream, args,
-            STATUS_BYTES if n == 1 else None)
+    if block_scores is None:
+        block_scores = q_idx.new_empty(
+            q_idx.shape[:3] + (_blocks(k_idx, block, block_table, max_kv),), dtype=_F32)
+    _run_q8("msa_block_scores_q8", "index", q_idx, workspace, stream,
+            (q_idx, k_idx, k_idx_scale, None, block_scores, causal, False, block, seq_lens,
+             block_table, max_kv))
     return block_scores
 
 
@@ -787,19 +708,17 @@ def msa_index_select_q8(q_idx, k_idx, k_idx_scale, *, block, topk, causal=True,
                         workspace: Workspace | None = None, stream=None):
     """msa_index_select over the 8-bit index key: block ids int32 [b, n_q, h, topk] (and the
     fp32 block scores if asked)."""
-    shape = b, n, h, d_idx = q_idx.shape
-    dev, planes, rows, cap, nblk, lead, lens, table = _cache_geometry(
-        k_idx, b, block, seq_lens, block_table, max_kv)
-    block_ids, ids = _made(q_idx, "block_ids", block_ids, (b, n, h, topk), _I32, dev)
-    block_scores, scores = _made(q_idx, "block_scores", block_scores, (b, n, h, nblk), _F32, dev,
-                                 return_scores)
-    params = _PARAMS.pack(
-        b, n, cap, h, h, 64, d_idx, block, topk, bool(causal), bool(force_own_block), 0.0, lens,
-        0, 0, 0, 0, 0, 0, 0, 0, 0, *_rows("q_idx", q_idx, shape, dev),
-        *_codes("k_idx", k_idx, (planes, rows, d_idx), dev), 0, 0, 0, *table)
-    args = (q_idx.data_ptr(), k_idx.data_ptr(),
-            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev), ids, scores)
-    _run_q8("msa_index_select_q8", MSA_OP_INDEX_SELECT_Q8, params, dev, workspace, stream, args)
+    lead = q_idx.shape[:3]
+    if block_ids is None:
+        block_ids = q_idx.new_empty(lead + (topk,), dtype=_I32)
+    elif block_ids.shape[-1] != topk:
+        raise ValueError("block_ids holds %d blocks, not %d" % (block_ids.shape[-1], topk))
+    if return_scores and block_scores is None:
+        block_scores = q_idx.new_empty(lead + (_blocks(k_idx, block, block_table, max_kv),),
+                                       dtype=_F32)
+    _run_q8("msa_index_select_q8", "index", q_idx, workspace, stream,
+            (q_idx, k_idx, k_idx_scale, block_ids, block_scores, causal, force_own_block, block,
+             seq_lens, block_table, max_kv))
     return (block_ids, block_scores) if return_scores else block_ids
 
 
@@ -809,24 +728,13 @@ def msa_sparse_attn_q8(q, k, v, k_scale, v_scale, block_ids, *, block, causal=Tr
                        stream=None):
     """msa_sparse_attn over the 8-bit cache: bf16 output [b, n_q, H, d] (and fp32 lse
     [b, n_q, H] if asked)."""
-    shape = b, n, H, d = q.shape
-    dev, planes, rows, cap, _, lead, lens, table = _cache_geometry(k, b, block, seq_lens,
-                                                                   block_table, max_kv)
-    h = k.shape[2]
-    topk = block_ids.shape[-1]
     if out is None:
         out = torch.empty_like(q)
-    lse, lse_ptr = _made(q, "lse", lse, (b, n, H), _F32, dev, return_lse)
-    cshape = (planes, rows, h, d)
-    params = _PARAMS.pack(
-        b, n, cap, H, h, d, 32, block, topk, bool(causal), 0, softmax_scale, lens,
-        *_rows("q", q, shape, dev), *_codes("k", k, cshape, dev), *_codes("v", v, cshape, dev),
-        0, 0, 0, 0, 0, *_rows("out", out, shape, dev), *table)
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            _dense("k_scale", k_scale, lead + (h,), _F32, dev),
-            _dense("v_scale", v_scale, lead + (h,), _F32, dev),
-            _dense("block_ids", block_ids, (b, n, h, topk), _I32, dev), out.data_ptr(), lse_ptr)
-    _run_q8("msa_sparse_attn_q8", MSA_OP_SPARSE_ATTN_Q8, params, dev, workspace, stream, args)
+    if return_lse and lse is None:
+        lse = q.new_empty(q.shape[:3], dtype=_F32)
+    _run_q8("msa_sparse_attn_q8", "attn", q, workspace, stream,
+            (q, k, v, k_scale, v_scale, block_ids, out, lse, causal, softmax_scale, block,
+             seq_lens, block_table, max_kv))
     return (out, lse) if return_lse else out
 
 
@@ -837,28 +745,20 @@ def msa_forward_q8(q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, *, bloc
                    workspace: Workspace | None = None, stream=None):
     """msa_forward over the 8-bit cache; returns out, plus (ids, scores, lse) when asked,
     in that order."""
-    shape = b, n, H, d = q.shape
-    dev, planes, rows, cap, nblk, lead, lens, table = _cache_geometry(k, b, block, seq_lens,
-                                                                      block_table, max_kv)
-    h, d_idx = k.shape[2], k_idx.shape[-1]
+    lead = q_idx.shape[:3]
     if out is None:
         out = torch.empty_like(q)
-    block_ids, ids = _made(q, "block_ids", block_ids, (b, n, h, topk), _I32, dev, return_ids)
-    block_scores, scores = _made(q, "block_scores", block_scores, (b, n, h, nblk), _F32, dev,
-                                 return_scores)
-    lse, lse_ptr = _made(q, "lse", lse, (b, n, H), _F32, dev, return_lse)
-    cshape = (planes, rows, h, d)
-    params = _PARAMS.pack(
-        b, n, cap, H, h, d, d_idx, block, topk, bool(causal), bool(force_own_block), softmax_scale,
-        lens, *_rows("q", q, shape, dev), *_codes("k", k, cshape, dev),
-        *_codes("v", v, cshape, dev), *_rows("q_idx", q_idx, (b, n, h, d_idx), dev),
-        *_codes("k_idx", k_idx, (planes, rows, d_idx), dev), *_rows("out", out, shape, dev), *table)
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_idx.data_ptr(), k_idx.data_ptr(),
-            _dense("k_scale", k_scale, lead + (h,), _F32, dev),
-            _dense("v_scale", v_scale, lead + (h,), _F32, dev),
-            _dense("k_idx_scale", k_idx_scale, lead, _F32, dev), out.data_ptr(), ids, scores,
-            lse_ptr)
-    _run_q8("msa_forward_q8", MSA_OP_FORWARD_Q8, params, dev, workspace, stream, args)
+    if return_ids and block_ids is None:
+        block_ids = q.new_empty(lead + (topk,), dtype=_I32)
+    if return_scores and block_scores is None:
+        block_scores = q.new_empty(lead + (_blocks(k_idx, block, block_table, max_kv),),
+                                   dtype=_F32)
+    if return_lse and lse is None:
+        lse = q.new_empty(q.shape[:3], dtype=_F32)
+    _run_q8("msa_forward_q8", "forward", q, workspace, stream,
+            (q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, out, block_ids, block_scores,
+             lse, topk, causal, force_own_block, softmax_scale, block, seq_lens, block_table,
+             max_kv))
     res = [out]
     if return_ids:
         res.append(block_ids)

@@ -593,6 +593,38 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, want[i]) for o in outs[i])
 
 
+def test_cache_larger_than_32_bit_offsets():
+    """2^31 codes and more in one tensor: the last row is written, scored, attended to and
+    read back."""
+    g = gen(51)
+    block, h, d, di, H, max_kv = 64, 8, 128, 128, 16, (1 << 21) + 130
+    c = msa.q8_cache(batch=1, max_kv=max_kv, h=h, d=d, d_idx=di, block=block)
+    assert c.k.numel() > 1 << 31
+    n, last = 70, (max_kv - 1) // block
+    new = rows(g, 1, n, h, d), rows(g, 1, n, h, d), rows(g, 1, n, di)
+    ws = msa.Workspace(DEV)
+    msa.msa_append_kv_q8(*c, *new, block=block, workspace=ws)
+    k, v, ki = msa.msa_read_kv_q8(*c, n=n, token_base=max_kv - n, block=block, workspace=ws)
+    for got, want in zip((k, v), new):
+        assert bool(((got - want).abs() <= want.abs() * 2.0 ** -4 + 2.0 ** -8).all())
+    q, qi = rows(g, 1, 1, H, d), rows(g, 1, 1, h, di)
+    ids = torch.tensor([last, last - 1], dtype=torch.int32, device=DEV).expand(1, 1, h, 2).contiguous()
+    out, lse = msa.msa_sparse_attn_q8(q, c.k, c.v, c.k_scale, c.v_scale, ids, block=block,
+                                      return_lse=True, workspace=ws)
+    ok(ws)
+    base = (last - 1) * block
+    local = torch.tensor([1, 0], dtype=torch.int32, device=DEV).expand(1, h, 2)
+    kk, vv, _ = msa.msa_read_kv_q8(*c, n=max_kv - base, token_base=base, block=block)
+    o, z, A, dx, total, N = q8_ref.attention(q[0].double(), kk[0].double(), vv[0].double(), local,
+                                             max_kv - base, block, d ** -0.5)
+    assert bool(((out[0].double() - o).abs() <= q8_ref.out_bound(o, A, dx, total, N, False)).all())
+    assert bool(((lse[0].double() - z).abs() <= q8_ref.lse_bound(z, dx)).all())
+    s = msa.msa_block_scores_q8(qi, c.k_idx, c.k_idx_scale, block=block)
+    want, mag = q8_ref.scores(qi[0].double(), ki[0].double()[-(max_kv - last * block):],
+                              max_kv - last * block, block)
+    assert bool(((s[0, 0, :, last].double() - want[0, :, 0]).abs() <= mag[0, :, 0] * 2.0 ** -16).all())
+
+
 # ------------------------------------------------------------------- random shapes
 @pytest.mark.parametrize("seed", range(24))
 def test_random_shapes(seed):

@@ -146,14 +146,21 @@ def test_binding_refuses_cpu_tensors_and_bad_geometry():
     assert pool.v.shape == (5, 16, 2, 64) and pool.k_idx_scale.shape == (5,)
 
 
-def test_packed_parameters_equal_the_structure():
-    p = params(n_q=3)
-    p.seq_lens, p.block_table, p.table_stride, p.num_pages = 4096, 8192, 17, 99
-    packed = msa._PARAMS.pack(
-        p.batch, p.n_q, p.max_kv, p.H, p.h, p.d, p.d_idx, p.block, p.topk, p.causal,
-        p.force_own_block, p.softmax_scale, p.seq_lens, *p.q_strides, *p.k_strides, *p.v_strides,
-        *p.qi_strides, *p.ki_strides, *p.o_strides, p.block_table, p.table_stride, p.num_pages)
-    assert packed == bytes(p)
+def test_binding_fails_loudly_without_its_extension(lib, monkeypatch):
+    monkeypatch.setattr(msa, "MARSHAL_PATH", "/nonexistent/_marshal.so")
+    with pytest.raises(RuntimeError, match="not built"):
+        msa._marshal_module()
+
+
+def test_marshalling_refuses_what_is_no_tensor(lib):
+    m = msa._marshal_module()
+    with pytest.raises(ValueError, match="arguments"):
+        m.attn(1, 2)
+    with pytest.raises(ValueError, match="must be a tensor"):
+        m.index(*range(13))
+    x = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        m.attn(x, x, x, x, x, x, x, None, True, 0.0, 64, None, None, None, None, 0)
 
 
 def test_reference_table_and_rounding():
