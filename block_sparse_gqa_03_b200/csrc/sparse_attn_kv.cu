@@ -41,8 +41,10 @@
 // the place of their widened form, and one warp widens them from the bottom up, so that
 // it never overwrites codes it has not read: no shared memory is needed for them.
 // Warp 0 does nothing else there (it walks the blocks, one ahead of the tiles), and
-// warps 2 and 3 gather Q.  A block's K scale joins the softmax scale of the tile and its
-// V scale the 1 / l of the output.
+// warps 2 and 3 gather Q.  A block's K scale joins the softmax scale of the tile; its V
+// scale joins the slot's weight in the merge, so that partial outputs are weighted means
+// of codes and are kept in f16 (bf16 ones doubled the rounding of the output: error
+// against 64 bits 0.0024 instead of 0.0017 of its norm).
 // Buffers: 2-4 Q tiles (released when S is computed), 2 K/V stages, and in tensor
 // memory 3-4 slots, each holding a tile's S and then its O, plus the two P
 // regions.  Every wait is bounded.
@@ -89,7 +91,7 @@ struct KvArgs {
   // head, so that a tile's output is one contiguous block; their log-sum-exps by
   // chunk-relative slot position p = (bt_rel * h + g) * topk + slot, so that a
   // query's are contiguous
-  uint16_t* part_o;        // [row][d] bf16
+  uint16_t* part_o;        // [row][d] bf16; of an 8-bit cache f16, in units of its V scale
   float* part_lse;         // [p][G]
   uint16_t* out;
   int64_t o_s0, o_s1, o_s2;
@@ -97,7 +99,9 @@ struct KvArgs {
   DeviceStatus* st;
   uint64_t wait_ns;
   KvPages pg;  // table == nullptr: contiguous K/V
-  const float *ks, *vs;  // 8-bit cache: scales per (block, KV head)
+  // 8-bit cache: scales per (block, KV head), and the V scale of every valid slot's block
+  const float *ks, *vs;
+  float* part_vs;          // [p], written by the scatter kernel
 };
 
 __device__ __forceinline__ int visible_from_length(const KvArgs& a, int L, int t) {
@@ -126,6 +130,14 @@ __device__ __forceinline__ bool slot_block(const KvArgs& a, int pos, int& b, int
     return false;
   }
   return (int64_t)beta * BLK < visible_limit(a, b, t);
+}
+
+// Scale of a block of an 8-bit cache; a page outside the pool reads as zeros.
+__device__ __forceinline__ float block_scale(const KvArgs& a, const float* scales, int b, int g,
+                                             int beta) {
+  int64_t plane = (int64_t)b * a.nblk + beta;
+  if (a.pg.table != nullptr) plane = kv_page(a.pg, b, beta, a.st);
+  return plane < 0 ? 1.f : __ldg(scales + plane * a.h + g);
 }
 
 // ----------------------------------------------------------- inverted index
@@ -209,9 +221,11 @@ __global__ void kv_scatter_kernel(KvArgs a, int BLK) {
       const int k = atomicAdd(&a.counts[j], 1);
       a.entries[a.offs[j] + k] = make_int2(pos, t);
       a.slot_row[pos] = (a.toffs[j] + k / a.qpt) * kRows + (k % a.qpt) * a.G;
+      if (a.vs != nullptr) a.part_vs[pos] = block_scale(a, a.vs, b, g, beta);
     } else {
       // no partial for this slot: the merge reads the marks, not the ids
       a.slot_row[pos] = -1;
+      if (a.vs != nullptr) a.part_vs[pos] = 0.f;
       for (int hh = 0; hh < a.G; ++hh)
         a.part_lse[(int64_t)pos * a.G + hh] = -__int_as_float(0x7f800000);
     }
@@ -331,13 +345,16 @@ __device__ __forceinline__ void widen_codes(uint32_t dst, int r0, int lane) {
   }
 }
 
-// Scales of a list's block; a page outside the pool reads as zeros.
-__device__ __forceinline__ void list_scales(const KvArgs& a, int b, int g, int beta, float& ks,
-                                            float& vs) {
-  int64_t plane = (int64_t)b * a.nblk + beta;
-  if (a.pg.table != nullptr) plane = kv_page(a.pg, b, beta, a.st);
-  ks = plane < 0 ? 1.f : __ldg(a.ks + plane * a.h + g);
-  vs = plane < 0 ? 1.f : __ldg(a.vs + plane * a.h + g);
+// Two partial outputs: bf16, or of an 8-bit cache f16 (they are weighted means of codes,
+// at most 448 in magnitude: three bits more than bf16 for the same bytes).
+template <bool Q8>
+__device__ __forceinline__ uint32_t pack_part(float lo, float hi) {
+  return Q8 ? q8::pack_f16(lo, hi) : pack_bf16(lo, hi);
+}
+template <bool Q8>
+__device__ __forceinline__ float2 unpack_part(uint32_t x) {
+  if constexpr (Q8) return q8::f16x2_floats(x);
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
 template <int D, int BLK, bool Q8>
@@ -690,19 +707,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       // with block 128 the look-ahead measured 4% slower (more spills) and the
       // position is loaded at the top of the tile's turn.
       constexpr int LA = BLK == 64 ? 2 : 0;
-      float sl_n = a.scale_log2, vs_n = 1.f;  // softmax scale and V scale of the tile
-      if constexpr (Q8) {
-        float ks;
-        list_scales(a, w.b, w.g, w.beta, ks, vs_n);
-        sl_n = a.scale_log2 * ks;
-      }
+      float sl_n = a.scale_log2;  // softmax scale of the tile
+      if constexpr (Q8) sl_n *= block_scale(a, a.ks, w.b, w.g, w.beta);
       auto row_visible = [&](int tile, int& t_row, int& beta_row, int& b_row) {
         const bool moved = w.advance(a, tile);
-        if (Q8 && moved) {
-          float ks;
-          list_scales(a, w.b, w.g, w.beta, ks, vs_n);
-          sl_n = a.scale_log2 * ks;
-        }
+        if (Q8 && moved) sl_n = a.scale_log2 * block_scale(a, a.ks, w.b, w.g, w.beta);
         t_row = -1;
         if (qi < w.count(a, tile)) t_row = __ldg(&a.entries[w.first(a, tile) + qi].y);
         beta_row = w.beta;
@@ -713,7 +722,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       for (int idx = sw; idx < n; idx += 2) {
         if (LA == 0) row_visible(tile0 + idx, t_n, beta_n, b_n);
         const int t_row = t_n, beta_row = beta_n, b_row = b_n;
-        const float sl = Q8 ? sl_n : a.scale_log2, vs = Q8 ? vs_n : 1.f;
+        const float sl = Q8 ? sl_n : a.scale_log2;
         if (LA > 0 && idx + LA < n) row_visible(tile0 + idx + LA, t_n, beta_n, b_n);
         int vis = BLK;
         if (t_row >= 0) {
@@ -768,7 +777,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         tc::tmem_wait_st();
         const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
         rstat[(idx & 3) * kRows + row] =
-            make_float2(l > 0.f ? (Q8 ? vs / l : 1.f / l) : 0.f, (ms != ninf && l > 0.f) ? (msafe + log2f(l)) * kLn2 : ninf);
+            make_float2(l > 0.f ? 1.f / l : 0.f, (ms != ninf && l > 0.f) ? (msafe + log2f(l)) * kLn2 : ninf);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
@@ -833,10 +842,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint32_t u0 = pack_bf16(v[8 * e] * rs.x, v[8 * e + 1] * rs.x);
-            const uint32_t u1 = pack_bf16(v[8 * e + 2] * rs.x, v[8 * e + 3] * rs.x);
-            const uint32_t u2 = pack_bf16(v[8 * e + 4] * rs.x, v[8 * e + 5] * rs.x);
-            const uint32_t u3 = pack_bf16(v[8 * e + 6] * rs.x, v[8 * e + 7] * rs.x);
+            const uint32_t u0 = pack_part<Q8>(v[8 * e] * rs.x, v[8 * e + 1] * rs.x);
+            const uint32_t u1 = pack_part<Q8>(v[8 * e + 2] * rs.x, v[8 * e + 3] * rs.x);
+            const uint32_t u2 = pack_part<Q8>(v[8 * e + 4] * rs.x, v[8 * e + 5] * rs.x);
+            const uint32_t u3 = pack_part<Q8>(v[8 * e + 6] * rs.x, v[8 * e + 7] * rs.x);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + swz128(lane, e)),
                          "r"(u0), "r"(u1), "r"(u2), "r"(u3)
                          : "memory");
@@ -877,7 +886,7 @@ __device__ __forceinline__ float pick_row(const float* m, int base, int rl) {
 // the group's valid slots by log-sum-exp weights; bf16 output and the natural-log
 // LSE.  A slot's GC partial rows are consecutive rows of its tile, read as one
 // contiguous piece, 16 bytes per lane.
-template <int D, int GC>
+template <int D, int GC, bool Q8>
 __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int BLK) {
   grid_dep_wait();
   grid_dep_launch();
@@ -934,17 +943,19 @@ __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int 
   for (int s0 = 0; s0 < a.topk; s0 += 32) {
     const int s = s0 + lane;
     const int prow = s < a.topk ? __ldg(a.slot_row + p0 + s) : -1;
+    const float pvs = Q8 && s < a.topk ? __ldg(a.part_vs + p0 + s) : 1.f;
     const bool ok = prow >= 0;
     const int cnt = min(32, a.topk - s0);
     for (int j0 = 0; j0 < cnt; j0 += U) {
       uint4 u[U][MI];
-      float l[U][MI];
+      float l[U][MI], sv[U];
       bool use[U];
 #pragma unroll
       for (int jj = 0; jj < U; ++jj) {
         const int j = min(j0 + jj, cnt - 1);
         use[jj] = j0 + jj < cnt && __shfl_sync(0xffffffffu, ok ? 1 : 0, j) != 0;
         const int rj = max(0, __shfl_sync(0xffffffffu, prow, j));
+        sv[jj] = Q8 ? __shfl_sync(0xffffffffu, pvs, j) : 1.f;
         const float* lp = a.part_lse + (p0 + s0 + j) * G;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
@@ -963,11 +974,13 @@ __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int 
           const bool live = l[jj][i] != ninf;
           const float w = live ? __expf(l[jj][i] - Mi[i]) : 0.f;
           den[i] += w;
+          const float wv = Q8 ? w * sv[jj] : w;
           const uint32_t x[4] = {u[jj][i].x, u[jj][i].y, u[jj][i].z, u[jj][i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            acc[i][2 * e] += live ? w * __uint_as_float(x[e] << 16) : 0.f;
-            acc[i][2 * e + 1] += live ? w * __uint_as_float(x[e] & 0xffff0000u) : 0.f;
+            const float2 y = unpack_part<Q8>(x[e]);
+            acc[i][2 * e] += live ? wv * y.x : 0.f;
+            acc[i][2 * e + 1] += live ? wv * y.y : 0.f;
           }
         }
     }
@@ -993,7 +1006,7 @@ __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int 
 // One warp per (query, head): merge the head's partials over the group's valid
 // slots by log-sum-exp weights; bf16 output and the natural-log LSE.  Lanes
 // take 32 slots at a time, so the loads of many partials are in flight at once.
-template <int D>
+template <int D, bool Q8>
 __global__ void __launch_bounds__(256) kv_combine_kernel(KvArgs a, int BLK) {
   grid_dep_wait();
   grid_dep_launch();
@@ -1051,9 +1064,10 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(KvArgs a, int BLK) {
         l = __ldg(a.part_lse + (p0 + s) * a.G + hi);
         prow = __ldg(a.slot_row + p0 + s);
       }
-      const float wgt = (prow >= 0 && l != ninf) ? __expf(l - M) : 0.f;
+      float wgt = (prow >= 0 && l != ninf) ? __expf(l - M) : 0.f;
       prow = prow >= 0 ? prow + hi : 0;  // row 0 stands in for none
       den += wgt;
+      if (Q8) wgt = s < a.topk ? wgt * __ldg(a.part_vs + p0 + s) : 0.f;
       // Loads are issued for every slot of the pass (a slot without a partial reads
       // row 0, which exists); such a slot contributes through a select, never a
       // multiply, so whatever that row holds cannot leak into the sum.  Sixteen slots
@@ -1078,11 +1092,13 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(KvArgs a, int BLK) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const bool use = wj[j] != 0.f;
-          acc[0] += use ? wj[j] * __uint_as_float(u[j].x << 16) : 0.f;
-          acc[1] += use ? wj[j] * __uint_as_float(u[j].x & 0xffff0000u) : 0.f;
+          const float2 y = unpack_part<Q8>(u[j].x);
+          acc[0] += use ? wj[j] * y.x : 0.f;
+          acc[1] += use ? wj[j] * y.y : 0.f;
           if constexpr (PER == 4) {
-            acc[2] += use ? wj[j] * __uint_as_float(u[j].y << 16) : 0.f;
-            acc[3] += use ? wj[j] * __uint_as_float(u[j].y & 0xffff0000u) : 0.f;
+            const float2 z = unpack_part<Q8>(u[j].y);
+            acc[2] += use ? wj[j] * z.x : 0.f;
+            acc[3] += use ? wj[j] * z.y : 0.f;
           }
         }
       }
@@ -1113,7 +1129,7 @@ struct KvPlan {
   int64_t rows, chunk_rows;
   int nchunks, qpt;
   int64_t nj, max_tiles;
-  size_t counts_off, offs_off, toffs_off, entries_off, slot_row_off, lse_off, o_off, total;
+  size_t counts_off, offs_off, toffs_off, entries_off, slot_row_off, vs_off, lse_off, o_off, total;
 };
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1129,7 +1145,7 @@ KvPlan plan_kv(const Shape& s) {
   const size_t row_bytes = (size_t)s.d * 2;
   const size_t fixed = (size_t)(p.nj + 1) * kRows * row_bytes;
   const size_t per_bt =
-      (size_t)s.h * s.topk * (12 + (size_t)s.G * 4 + kRows * row_bytes / p.qpt + 1);
+      (size_t)s.h * s.topk * (12 + (s.kv8 ? 4 : 0) + (size_t)s.G * 4 + kRows * row_bytes / p.qpt + 1);
   int64_t cr = fixed < kKvPartialBudget ? (int64_t)((kKvPartialBudget - fixed) / per_bt) : 1;
   cr = cr < 1 ? 1 : cr;
   const int64_t max_slots = (int64_t)1 << 30;  // chunk-relative positions are int32
@@ -1149,6 +1165,8 @@ KvPlan plan_kv(const Shape& s) {
   off = up256(off + slots * 8);
   p.slot_row_off = off;
   off = up256(off + slots * 4);
+  p.vs_off = off;
+  if (s.kv8) off = up256(off + slots * 4);
   p.lse_off = off;
   off = up256(off + slots * s.G * 4);
   p.o_off = off;
@@ -1193,10 +1211,10 @@ cudaError_t run_kv(const Shape& s, KvArgs& a, const KvPlan& p, const CUtensorMap
     // Groups of 8 heads: one warp per (query, group) (measured 4% faster at G = 8,
     // no faster at G = 6, where a warp per (query, head) has more loads in flight).
     if (s.G == 8)
-      kv_combine_group_kernel<D, 8><<<(unsigned)(((int64_t)a.nbt * s.h + 7) / 8), 256, 0, stream>>>(
+      kv_combine_group_kernel<D, 8, Q8><<<(unsigned)(((int64_t)a.nbt * s.h + 7) / 8), 256, 0, stream>>>(
           a, BLK);
     else
-      kv_combine_kernel<D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a, BLK);
+      kv_combine_kernel<D, Q8><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a, BLK);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
   return cudaSuccess;
@@ -1258,6 +1276,7 @@ cudaError_t launch_kv_attn(const Shape& s, const CUtensorMap& tmq, const CUtenso
   if (!make_rows_map(&tmo, a.part_o, p.max_tiles * kRows, s.d)) return cudaErrorInvalidValue;
   a.ks = s.ks;
   a.vs = s.vs;
+  a.part_vs = reinterpret_cast<float*>(w + p.vs_off);
 #define MSA_KV_CASE(D_, B_)                                                          \
   if (s.d == D_ && s.block == B_)                                                    \
     return s.kv8 ? run_kv<D_, B_, true>(s, a, p, tmq, tmk, tmv, tmo, w, stream)      \
