@@ -615,15 +615,20 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
 }
 
 // ------------------------------------------------------- one CTA per row
-constexpr int kRowsNC = 4;
+// Rows of fewer than 1024 listed tokens take two consumer warps and up to five CTAs per
+// SM (the many rows of a prompt with small blocks: what counts is how many of them are
+// under way), longer ones four warps and two CTAs (decode of many sequences: deeper
+// buffers).  1998 rows of 8 x 32 tokens 23.5 us with two warps, 39.4 us with four; 768
+// rows of 64 x 64 tokens 128 us with four, 175 us with two.
+constexpr int kShortRow = 1024;
 
-template <class WS>
-__global__ void __launch_bounds__((kRowsNC + 1) * 32, 2)
+template <int NC, class WS>
+__global__ void __launch_bounds__((NC + 1) * 32, NC == 2 ? 5 : 2)
     sparse_attn_rows_q8_kernel(const __grid_constant__ CUtensorMap tmk,
                                const __grid_constant__ CUtensorMap tmv, AttnArgs a) {
   grid_dep_wait();
   grid_dep_launch();
-  constexpr int NC = kRowsNC, D = WS::kD, LD = WS::kLd;
+  constexpr int D = WS::kD, LD = WS::kLd;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -813,6 +818,9 @@ __global__ void __launch_bounds__((NC + 2) * 32, 1)
 // Tokens per stage: 16 KB at most, so that there are more stages than consumer warps.
 int stage_tokens(const Shape& s) { return s.block < 64 ? s.block : 64; }
 
+// Consumer warps of the one-CTA-per-row kernel.
+int rows_warps(const Shape& s) { return (int64_t)s.topk * s.block < kShortRow ? 2 : 4; }
+
 constexpr int kStreamNC = 6;    // consumer warps of the streaming kernel
 constexpr int kMaxList = 4096;  // entries a streaming CTA compacts up front
 
@@ -887,9 +895,10 @@ AttnPlan plan_attn_q8(const Shape& s) {
     pl.merge_off = pl.stages * pl.stage_bytes;
     pl.region_bytes = pl.merge_off + merge_r;
   } else {
-    // two CTAs per SM
-    pl.stages = min(8, (int)((100u * 1024u) / pl.stage_bytes));
-    pl.region_bytes = max(pl.stages * pl.stage_bytes, merge_bytes(kRowsNC));
+    const int nc = rows_warps(s);
+    pl.stages = nc == 2 ? max(2, min(4, (int)((40u * 1024u) / pl.stage_bytes)))
+                        : min(8, (int)((100u * 1024u) / pl.stage_bytes));
+    pl.region_bytes = max(pl.stages * pl.stage_bytes, merge_bytes(nc));
     pl.region_bytes = (pl.region_bytes + 15) & ~15u;
     pl.merge_off = 0;
     pl.ctas = (int)rows_g;
@@ -920,9 +929,11 @@ cudaError_t run_attn_q8(const Shape& s, const AttnPlan& pl, const void* k, const
     return with_state(s, [&](auto ws) {
       return launch(sparse_attn_stream_q8_kernel<kStreamNC, decltype(ws)>, (kStreamNC + 2) * 32);
     });
-  return with_state(s, [&](auto ws) {
-    return launch(sparse_attn_rows_q8_kernel<decltype(ws)>, (kRowsNC + 1) * 32);
-  });
+  if (rows_warps(s) == 2)
+    return with_state(
+        s, [&](auto ws) { return launch(sparse_attn_rows_q8_kernel<2, decltype(ws)>, 3 * 32); });
+  return with_state(
+      s, [&](auto ws) { return launch(sparse_attn_rows_q8_kernel<4, decltype(ws)>, 5 * 32); });
 }
 
 }  // namespace msa
