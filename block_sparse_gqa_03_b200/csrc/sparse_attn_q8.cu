@@ -482,7 +482,7 @@ template <int D, int NC, int LD, int NT, class Sync>
 __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, const RowGeo& rg,
                                         float* mo, float* mm, float* ml, int* flag, int tid,
                                         Sync sync) {
-  constexpr int U = 4;  // items of four dims per thread whose loads are under way together
+  constexpr int U = NT == 32 ? 4 : 2;  // items per thread whose loads are under way together
   const int c_first = cur * a.topk / a.per;
   const int nseg = ((cur + 1) * a.topk - 1) / a.per - c_first + 1;
   const int seg = c - c_first;
@@ -508,68 +508,8 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
   }
   sync();
   const bool fast = nseg > 1 && seg == 0 && *flag == nseg - 1;
-  const int64_t orow = rg.b * a.o_s0 + (int64_t)rg.t * a.o_s1 + (int64_t)(rg.g * a.G) * a.o_s2;
-  // The row's output from its segments: sp0 = 1 with this CTA's (segment 0) from the
-  // stash, sp0 = 0 all from the partials.
-  auto merge_segments = [&](int sp0) {
-    if (tid < a.G) {  // maximum and 1 / sum over the segments (of warps 2 and 3)
-      const float* pl = a.part_lse + pr_g + (int64_t)tid * a.smax;
-      float M = sp0 ? ml[16 + tid] : ninf;
-      for (int sp = sp0; sp < nseg; ++sp) M = fmaxf(M, __ldcg(pl + sp));
-      float den = sp0 && M != ninf ? exp2f((ml[16 + tid] - M) * kLog2e) : 0.f;
-      for (int sp = sp0; sp < nseg; ++sp)
-        den += M != ninf ? exp2f((__ldcg(pl + sp) - M) * kLog2e) : 0.f;
-      ml[32 + tid] = M;
-      ml[48 + tid] = M != ninf ? 1.f / den : 0.f;
-      if (a.lse)
-        a.lse[(int64_t)rg.bt * a.H + rg.g * a.G + tid] = M != ninf ? M + log2f(den) * kLn2 : ninf;
-    }
-    sync();
-#pragma unroll 1
-    for (int x0 = tid; x0 < total; x0 += U * NT) {
-      float4 acc[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int x = x0 + i * NT;
-        if (sp0 && x < total) {
-          const int row = x / (D / 4);
-          const float w = ml[32 + row] != ninf ? exp2f((ml[16 + row] - ml[32 + row]) * kLog2e) : 0.f;
-          const float4 o = *reinterpret_cast<const float4*>(mo + row * LD + (x % (D / 4)) * 4);
-          acc[i] = make_float4(w * o.x, w * o.y, w * o.z, w * o.w);
-        }
-      }
-#pragma unroll 1
-      for (int sp = sp0; sp < nseg; ++sp) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int x = min(x0 + i * NT, total - 1), row = x / (D / 4);
-          const int64_t pr = pr_g + (int64_t)row * a.smax + sp;
-          const float l = __ldcg(a.part_lse + pr);
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * D) + x % (D / 4));
-          const float w = ml[32 + row] != ninf ? exp2f((l - ml[32 + row]) * kLog2e) : 0.f;
-          acc[i].x += w * o.x;
-          acc[i].y += w * o.y;
-          acc[i].z += w * o.z;
-          acc[i].w += w * o.w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int x = x0 + i * NT, row = x / (D / 4);
-        if (x < total) {
-          const float inv = ml[48 + row];
-          *reinterpret_cast<uint2*>(a.out + orow + row * a.o_s2 + (x % (D / 4)) * 4) =
-              make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv),
-                         pack_bf16(acc[i].z * inv, acc[i].w * inv));
-        }
-      }
-    }
-  };
-  // this CTA's segment: to the output, to the partials, or (fast) over warp 0's stash
-#pragma unroll 1
-  for (int x = tid; x < total; x += NT) {
-    const int row = x / (D / 4), dim = (x % (D / 4)) * 4;
+  // the warps' states merged: four dims of a head row
+  auto stashed = [&](int row, int dim) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < NC; ++w) {
@@ -581,13 +521,84 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
       v.w += f * o.w;
     }
     const float inv = ml[row];
-    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    return make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  };
+  const int64_t orow = rg.b * a.o_s0 + (int64_t)rg.t * a.o_s1 + (int64_t)(rg.g * a.G) * a.o_s2;
+  auto put = [&](int row, int dim, const float4& v, float l) {
+    *reinterpret_cast<uint2*>(a.out + orow + row * a.o_s2 + dim) =
+        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    if (dim == 0 && a.lse) a.lse[(int64_t)rg.bt * a.H + rg.g * a.G + row] = l;
+  };
+  // The row's output from its segments, four dims per thread: segment 0 (this CTA's, from
+  // the stash, when `own`; else its partial) and then the others in their order.  Two
+  // segments of U items are loaded together, so a row of two or three takes one round
+  // trip to L2.
+  auto merge_segments = [&](bool own) {
+#pragma unroll 1
+    for (int x0 = tid; x0 < total; x0 += U * NT) {
+      float M[U], den[U];
+      float4 acc[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int x = min(x0 + i * NT, total - 1), row = x / (D / 4), dim = (x % (D / 4)) * 4;
+        const int64_t pr = pr_g + (int64_t)row * a.smax;
+        acc[i] = own ? stashed(row, dim)
+                     : __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * D + dim));
+        M[i] = own ? ml[16 + row] : __ldcg(a.part_lse + pr);
+        den[i] = M[i] != ninf ? 1.f : 0.f;  // a segment without a key holds zeros
+      }
+#pragma unroll 1
+      for (int sp = 1; sp < nseg; sp += 2) {
+        float l[U][2];
+        float4 o[U][2];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int x = min(x0 + i * NT, total - 1), row = x / (D / 4), dim = (x % (D / 4)) * 4;
+            const int64_t pr = pr_g + (int64_t)row * a.smax + min(sp + k, nseg - 1);
+            l[i][k] = __ldcg(a.part_lse + pr);
+            o[i][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * D + dim));
+            if (sp + k >= nseg) l[i][k] = ninf;
+          }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const float Mn = fmax3(M[i], l[i][0], l[i][1]);
+          if (Mn == ninf) continue;
+          const float c = exp2f((M[i] - Mn) * kLog2e);
+          const float w0 = exp2f((l[i][0] - Mn) * kLog2e), w1 = exp2f((l[i][1] - Mn) * kLog2e);
+          M[i] = Mn;
+          den[i] = den[i] * c + w0 + w1;
+          acc[i].x = acc[i].x * c + w0 * o[i][0].x + w1 * o[i][1].x;
+          acc[i].y = acc[i].y * c + w0 * o[i][0].y + w1 * o[i][1].y;
+          acc[i].z = acc[i].z * c + w0 * o[i][0].z + w1 * o[i][1].z;
+          acc[i].w = acc[i].w * c + w0 * o[i][0].w + w1 * o[i][1].w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int x = x0 + i * NT;
+        const float inv = M[i] != ninf ? 1.f / den[i] : 0.f;
+        if (x < total)
+          put(x / (D / 4), (x % (D / 4)) * 4,
+              make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv),
+              M[i] != ninf ? M[i] + log2f(den[i]) * kLn2 : ninf);
+      }
+    }
+  };
+  // (the row's counter goes back to zero, for the next call, with the merge)
+  if (fast) {
+    if (tid == 0) a.counters[cur] = 0;
+    merge_segments(true);
+    return;
+  }
+  // this CTA's segment: the output, or a partial
+#pragma unroll 1
+  for (int x = tid; x < total; x += NT) {
+    const int row = x / (D / 4), dim = (x % (D / 4)) * 4;
+    const float4 v = stashed(row, dim);
     if (nseg == 1) {
-      *reinterpret_cast<uint2*>(a.out + orow + row * a.o_s2 + dim) =
-          make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-      if (dim == 0 && a.lse) a.lse[(int64_t)rg.bt * a.H + rg.g * a.G + row] = ml[16 + row];
-    } else if (fast) {
-      *reinterpret_cast<float4*>(mo + row * LD + dim) = v;  // read and written by this thread
+      put(row, dim, v, ml[16 + row]);
     } else {
       const int64_t pr = pr_g + (int64_t)row * a.smax + seg;
       *reinterpret_cast<float4*>(a.part_o + pr * D + dim) = v;
@@ -595,12 +606,6 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
     }
   }
   if (nseg == 1) return;
-  // (the row's counter goes back to zero, for the next call, with the merge)
-  if (fast) {
-    if (tid == 0) a.counters[cur] = 0;
-    merge_segments(1);
-    return;
-  }
   // One thread publishes the partial (the other threads' stores ordered before its
   // atomic by the barrier) and learns whether it is the row's last; the atomic also
   // orders the other CTAs' partials before the loads above.
@@ -611,7 +616,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
     if (f == nseg - 1) a.counters[cur] = 0;
   }
   sync();
-  if (*flag == nseg - 1) merge_segments(0);
+  if (*flag == nseg - 1) merge_segments(false);
 }
 
 // ------------------------------------------------------- one CTA per row
@@ -714,7 +719,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, 1)
   const uint32_t sbase = smem_u32(smem);
   float* mo = reinterpret_cast<float*>(smem + a.merge_off);  // [NC][G][LD]
   float* mm = mo + NC * a.G * LD;                             // [NC][16]
-  float* ml = mm + NC * 16;                                   // [NC][16], NC >= 4
+  float* ml = mm + NC * 16;                                   // [NC][16]
   int* flag = reinterpret_cast<int*>(ml + NC * 16);           // [2]: consumers, finishing warp
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + a.region_bytes);
   int32_t* list = reinterpret_cast<int32_t*>(bars + 2 * a.stages);
