@@ -172,6 +172,9 @@ msa_status_t check_attn_args(const Shape& s, const void* q, const void* k, const
 // ---- 8-bit cache: rows of one-byte codes, 16-byte aligned; fp32 scales
 bool good_stride16(int64_t st) { return st > 0 && (st % 16) == 0; }
 
+// Grids and item counts of the 8-bit kernels are 32-bit.
+bool fits_grid(int64_t n) { return n <= (int64_t)INT32_MAX - 4096; }
+
 bool good_codes(const void* codes, const float* scale, const int64_t* st, int d) {
   return codes != nullptr && scale != nullptr && aligned16(codes) &&
          (reinterpret_cast<uintptr_t>(scale) & 3u) == 0 && good_stride16(st[0]) &&
@@ -189,7 +192,7 @@ msa_status_t check_select_args_q8(const Shape& s, const void* q_idx, const void*
   if (!q_idx || !aligned16(q_idx) || check_strides3(s.qi_s) != MSA_OK || s.qi_s[2] < s.d_idx ||
       !good_idx_codes(s, k_idx, scale))
     return MSA_ERR_INVALID_ARG;
-  return MSA_OK;
+  return fits_grid((int64_t)s.batch * s.nblk) ? MSA_OK : MSA_ERR_UNSUPPORTED;
 }
 
 msa_status_t check_attn_args_q8(const Shape& s, const void* q, const void* k, const void* v,
@@ -612,6 +615,8 @@ msa_status_t msa_append_kv_q8(const msa_params_t* params, const msa_bf16_t* k_ne
       (v_new && (!aligned16(v_new) || !good_codes(v, v_scale, s.v_s, s.d))) ||
       (k_idx_new && (!aligned16(k_idx_new) || !good_idx_codes(s, k_idx, k_idx_scale))))
     return MSA_ERR_INVALID_ARG;
+  if (!fits_grid((int64_t)s.batch * (s.n_q / s.block + 2) * (2 * s.h + 1)))
+    return MSA_ERR_UNSUPPORTED;
   if ((rc = check_ws(s, MSA_OP_APPEND_KV_Q8, workspace, workspace_bytes)) != MSA_OK) return rc;
   const msa::Q8Cache c = {k, v, k_idx, k_scale, v_scale, k_idx_scale};
   return cuda_status(msa::launch_append_kv_q8(s, k_new, v_new, k_idx_new, c,
@@ -633,6 +638,7 @@ msa_status_t msa_read_kv_q8(const msa_params_t* params, const msa_e4m3_t* k, con
       (v_out && (!aligned16(v_out) || !good_codes(v, v_scale, s.v_s, s.d))) ||
       (k_idx_out && (!aligned16(k_idx_out) || !good_idx_codes(s, k_idx, k_idx_scale))))
     return MSA_ERR_INVALID_ARG;
+  if (!fits_grid((int64_t)s.batch * (s.n_q / 16 + 2))) return MSA_ERR_UNSUPPORTED;
   if ((rc = check_ws(s, MSA_OP_READ_KV_Q8, workspace, workspace_bytes)) != MSA_OK) return rc;
   const msa::Q8Cache c = {const_cast<msa_e4m3_t*>(k),     const_cast<msa_e4m3_t*>(v),
                           const_cast<msa_e4m3_t*>(k_idx), const_cast<float*>(k_scale),

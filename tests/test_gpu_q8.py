@@ -296,6 +296,11 @@ ATTN_CASES = [
     (300, 16, 1, 128, 128, 3, 500, [500, 300], True),
     (310, 10, 2, 64, 128, 2, 310, [310, 77], False),
     (200, 48, 16, 128, 64, 3, 256, [256], True),
+    # many sequences: one CTA per row, short and long lists, groups on both sides of 8
+    (1, 16, 8, 64, 64, 3, 200, [200 - i for i in range(80)], True),
+    (1, 24, 8, 128, 64, 20, 1500, [1500 - 19 * i for i in range(75)], True),
+    (1, 48, 4, 128, 128, 9, 1300, [1300 - 8 * i for i in range(150)], True),
+    (1, 12, 4, 64, 16, 70, 1200, [1200 - 7 * i for i in range(160)], True),
 ]
 
 
@@ -623,6 +628,58 @@ def test_cache_larger_than_32_bit_offsets():
     want, mag = q8_ref.scores(qi[0].double(), ki[0].double()[-(max_kv - last * block):],
                               max_kv - last * block, block)
     assert bool(((s[0, 0, :, last].double() - want[0, :, 0]).abs() <= mag[0, :, 0] * 2.0 ** -16).all())
+
+
+def test_codes_as_bytes_and_a_padded_index_key():
+    """uint8 tensors hold the same codes; index-key rows may lie apart."""
+    g = gen(52)
+    c, _ = random_cache(g, batch=2, max_kv=200, h=2, d=64, d_idx=64, block=32, paged=False)
+    wide = torch.zeros((2, 200, 96), dtype=torch.uint8, device=DEV)
+    wide[:, :, :64] = u8(c.k_idx)
+    q, ids = rows(g, 2, 1, 4, 64), ids_for(g, [200, 200], 1, 2, 7, 32, 3)
+    for n in (1, 20):
+        qi = rows(g, 2, n, 2, 64)
+        want = msa.msa_block_scores_q8(qi, c.k_idx, c.k_idx_scale, block=32)
+        got = msa.msa_block_scores_q8(qi, wide[:, :, :64], c.k_idx_scale, block=32)
+        assert torch.equal(want, got)
+    want = msa.msa_sparse_attn_q8(q, c.k, c.v, c.k_scale, c.v_scale, ids, block=32)
+    got = msa.msa_sparse_attn_q8(q, u8(c.k), u8(c.v), c.k_scale, c.v_scale, ids, block=32)
+    assert torch.equal(want, got)
+
+
+def test_refusals_name_the_argument():
+    g = gen(53)
+    c, table = random_cache(g, batch=2, max_kv=64, h=2, d=64, d_idx=32, block=16, paged=False)
+    q, ids = rows(g, 2, 1, 4, 64), torch.zeros((2, 1, 2, 3), dtype=torch.int32, device=DEV)
+    new = rows(g, 2, 1, 2, 64)
+    a = [q, c.k, c.v, c.k_scale, c.v_scale, ids]
+    for i, bad, word in ((0, q.float(), "q"), (0, rows(g, 3, 1, 4, 64), "sequences"),
+                         (1, c.k.float(), "k"), (2, c.v[:, :, :1], "v"),
+                         (3, c.k_scale.half(), "k_scale"), (4, c.v_scale[:, :-1], "v_scale"),
+                         (5, ids.long(), "block_ids"), (5, ids[:, :, :1], "block_ids")):
+        args = list(a)
+        args[i] = bad
+        with pytest.raises(ValueError, match=word):
+            msa.msa_sparse_attn_q8(*args, block=16)
+    with pytest.raises(ValueError, match="seq_lens"):
+        msa.msa_sparse_attn_q8(*a, block=16, seq_lens=torch.zeros(2, device=DEV))
+    with pytest.raises(ValueError, match="k_new"):
+        msa.msa_append_kv_q8(*c, new.transpose(2, 3), block=16)
+    with pytest.raises(ValueError, match="max_kv"):
+        msa.msa_append_kv_q8(*c, new, block=16, max_kv=63)
+    with pytest.raises(ValueError, match="max_kv"):
+        msa.msa_append_kv_q8(*c, new, block=16, block_table=torch.zeros((2, 4), dtype=torch.int32,
+                                                                       device=DEV))
+    with pytest.raises(ValueError, match="page"):  # the pool's pages are not of `block` tokens
+        msa.msa_append_kv_q8(*c, new, block=16, max_kv=64,
+                             block_table=torch.zeros((2, 4), dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError, match="rows"):
+        msa.msa_read_kv_q8(*c, n=3, block=16, k_out=new, v_out=new, k_idx_out=new)
+    with pytest.raises(msa.MsaError):
+        msa.msa_read_kv_q8(*c, n=10, token_base=60, block=16)
+    with pytest.raises(msa.MsaError):  # strides of 24 bytes
+        msa.msa_block_scores_q8(rows(g, 2, 1, 1, 32), torch.zeros(
+            (2, 64, 40), dtype=torch.uint8, device=DEV)[:, :, :32], c.k_idx_scale, block=16)
 
 
 # ------------------------------------------------------------------- random shapes
