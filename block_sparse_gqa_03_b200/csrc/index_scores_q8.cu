@@ -5,12 +5,12 @@
 //
 // What bounds it: L_b * d_idx bytes of HBM per sequence, half of the bf16 scan's.
 // Persistent, one CTA per SM, each an equal contiguous share of the flattened
-// (sequence, block) items; warp w takes items w, w + 8, ...  Each warp streams its own
+// (sequence, block) items; warp w takes items w, w + 12, ...  Each warp streams its own
 // items: it resolves 32 of them at a time (one per lane: sequence, block, page,
 // scale), its lane 0 issues the TMA loads (rows of d_idx bytes, swizzled by the row
 // size) into the warp's private ring of stages and refills a stage as soon as the
-// warp has read it.  One producer warp for all eight, as in the bf16 scan, issues an
-// 8 KB block every 250 ns at best: 61.7 us against 53.7 us for 16 x 128K tokens of 128
+// warp has read it.  One producer warp for all of them, as in the bf16 scan, issues an
+// 8 KB block every 250 ns at best: 61.7 us against 52.5 us for 16 x 128K tokens of 128
 // dims (41.7 us of HBM time).
 //
 // A code row is read by ldmatrix as pairs of bytes: a lane's 32-bit register holds
@@ -40,7 +40,7 @@ struct ScanQ8Args {
   KvPages pg;
 };
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 12;  // 8: 53.4 us for the scan above, 12: 52.5, 16: 53.9
 constexpr int kMaxDepth = 16;  // stages of a warp
 
 __device__ __forceinline__ int seq_blocks(const ScanQ8Args& a, int b) {
@@ -286,7 +286,7 @@ cudaError_t run_scan(const Shape& s, const uint8_t* k_idx, ScanQ8Args& a, cudaSt
   a.stage_bytes = (uint32_t)DI * (uint32_t)a.unit;
   const size_t fixed = 1024, per_stage = a.stage_bytes + 24;
   a.depth = min(kMaxDepth, (int)(((size_t)max_smem_optin() - fixed) / (per_stage * kWarps)));
-  if (a.depth < 1) return cudaErrorInvalidValue;  // 8 KB stages at most: 3 fit
+  if (a.depth < 1) return cudaErrorInvalidValue;  // 8 KB stages at most: 2 fit
   const size_t smem = fixed + (size_t)(a.depth * kWarps) * per_stage;
   cudaError_t err = cudaFuncSetAttribute(index_scan_q8_kernel<DI, NT, MT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
