@@ -330,8 +330,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-    if (srow != nullptr && a.fill_tail && row_ok && ng < ng_valid && sp == a.n_split - 1)
-      for (int beta = n_all * bpt; beta < a.nblk; ++beta) srow[beta] = ninf;
+    if (a.scores != nullptr && a.fill_tail && ng < ng_valid) {
+      // this CTA's share of the blocks no query of the tile sees, a row of the warp at a
+      // time so that the stores are contiguous
+      const int tail = n_all * bpt, len = max(0, a.nblk - tail);
+      const int c0 = tail + (int)((int64_t)len * sp / a.n_split);
+      const int c1 = tail + (int)((int64_t)len * (sp + 1) / a.n_split);
+      for (int r = 0; r < 32 && t0 + quarter * 32 + r < a.n_q; ++r) {
+        const int64_t tr = (int64_t)b * a.n_q + t0 + quarter * 32 + r;
+        float* dst = a.scores + (tr * a.h + gp * kNG + ng) * (int64_t)a.nblk;
+        for (int beta = c0 + lane; beta < c1; beta += 32) dst[beta] = ninf;
+      }
+    }
     if constexpr (TOPK) {
       if (row_ok && ng < ng_valid) {
         // the kept ids (empty entries are 0xffff and sort last) and the forced own
@@ -404,7 +414,7 @@ cudaError_t run_tc(const Shape& s, const uint16_t* q_idx, const uint16_t* k_idx,
   // Few query tiles (a chunk of a prompt, a short batch): the key tiles are split over
   // CTAs up to one wave, at least 8 tiles each (every block's score depends on its own
   // tile alone; the streaming top-k needs them all in one CTA).  2048 queries, 4 groups
-  // of 64 dims, 32K keys: 32 CTAs took 181 us, 4 shares each SPLITUS us.
+  // of 64 dims, 32K keys: 32 CTAs took 181 us, 4 shares each 46 us.
   const int64_t ctas = (int64_t)s.batch * a.n_gpairs * a.n_mtiles;
   const int tiles = (s.max_kv + kKT - 1) / kKT;
   a.n_split = TOPK ? 1 : (int)max((int64_t)1, min(num_sms() / ctas, (int64_t)tiles / 8));
