@@ -24,6 +24,8 @@
 // block arrives and 4 to 6 us after the last one, in the rows' merges.
 // A block's K scale joins the softmax scale of its scores and its V scale the fp32
 // accumulation of its product, so that neither is rounded to 16 bits.
+#include <math.h>
+
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -482,7 +484,8 @@ template <int D, int NC, int LD, int NT, class Sync>
 __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, const RowGeo& rg,
                                         float* mo, float* mm, float* ml, int* flag, int tid,
                                         Sync sync) {
-  constexpr int U = NT == 32 ? 4 : 2;  // items per thread whose loads are under way together
+  // items per thread, and segments of each, whose loads are under way together
+  constexpr int U = NT == 32 ? 4 : 2, K = NT == 32 ? 2 : 4;
   const int c_first = cur * a.topk / a.per;
   const int nseg = ((cur + 1) * a.topk - 1) / a.per - c_first + 1;
   const int seg = c - c_first;
@@ -530,9 +533,8 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
     if (dim == 0 && a.lse) a.lse[(int64_t)rg.bt * a.H + rg.g * a.G + row] = l;
   };
   // The row's output from its segments, four dims per thread: segment 0 (this CTA's, from
-  // the stash, when `own`; else its partial) and then the others in their order.  Two
-  // segments of U items are loaded together, so a row of two or three takes one round
-  // trip to L2.
+  // the stash, when `own`; else its partial) and then the others in their order, K at a
+  // time: a row of up to K + 1 segments takes one round trip to L2.
   auto merge_segments = [&](bool own) {
 #pragma unroll 1
     for (int x0 = tid; x0 < total; x0 += U * NT) {
@@ -548,13 +550,13 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
         den[i] = M[i] != ninf ? 1.f : 0.f;  // a segment without a key holds zeros
       }
 #pragma unroll 1
-      for (int sp = 1; sp < nseg; sp += 2) {
-        float l[U][2];
-        float4 o[U][2];
+      for (int sp = 1; sp < nseg; sp += K) {
+        float l[U][K];
+        float4 o[U][K];
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < K; ++k) {
             const int x = min(x0 + i * NT, total - 1), row = x / (D / 4), dim = (x % (D / 4)) * 4;
             const int64_t pr = pr_g + (int64_t)row * a.smax + min(sp + k, nseg - 1);
             l[i][k] = __ldcg(a.part_lse + pr);
@@ -563,16 +565,26 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
           }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          const float Mn = fmax3(M[i], l[i][0], l[i][1]);
+          float Mn = M[i];
+#pragma unroll
+          for (int k = 0; k < K; ++k) Mn = fmaxf(Mn, l[i][k]);
           if (Mn == ninf) continue;
           const float c = exp2f((M[i] - Mn) * kLog2e);
-          const float w0 = exp2f((l[i][0] - Mn) * kLog2e), w1 = exp2f((l[i][1] - Mn) * kLog2e);
           M[i] = Mn;
-          den[i] = den[i] * c + w0 + w1;
-          acc[i].x = acc[i].x * c + w0 * o[i][0].x + w1 * o[i][1].x;
-          acc[i].y = acc[i].y * c + w0 * o[i][0].y + w1 * o[i][1].y;
-          acc[i].z = acc[i].z * c + w0 * o[i][0].z + w1 * o[i][1].z;
-          acc[i].w = acc[i].w * c + w0 * o[i][0].w + w1 * o[i][1].w;
+          den[i] *= c;
+          acc[i].x *= c;
+          acc[i].y *= c;
+          acc[i].z *= c;
+          acc[i].w *= c;
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const float w = exp2f((l[i][k] - Mn) * kLog2e);
+            den[i] += w;
+            acc[i].x += w * o[i][k].x;
+            acc[i].y += w * o[i][k].y;
+            acc[i].z += w * o[i][k].z;
+            acc[i].w += w * o[i][k].w;
+          }
         }
       }
 #pragma unroll
@@ -883,6 +895,11 @@ AttnPlan plan_attn_q8(const Shape& s) {
     // an even share, but a block for each consumer warp: in a small problem, finer shares
     // only add partials to merge
     pl.per = max((int)((pl.total + pl.ctas - 1) / pl.ctas), min(kStreamNC, s.topk));
+    // A longer share also means fewer segments for a row's last CTA to merge, one after
+    // the other: per * t + topk / per * 0.18 us is least at sqrt(topk * 0.18 / t), t the
+    // time a block takes its SM (its bytes at 44 GB/s, 0.1 us at least).
+    const double t = fmax(0.1, 2.0 * s.d * s.block / 44000.0);
+    pl.per = max(pl.per, (int)ceil(sqrt(s.topk * 0.18 / t)));
     // Whole rows where that adds at most a block per warp (2 us): a split row's partials
     // are published and merged in 3 to 4 us.  (One sequence of 2 groups with 8 blocks:
     // SMALLA us with split rows, SMALLB us without.)
