@@ -616,11 +616,17 @@ def _run_q8(what, entry, like, workspace, stream, args):
     dev = like.get_device()
     if dev < 0:
         raise ValueError("the 8-bit cache calls need CUDA tensors")
+    if stream is not None:
+        # made current: its capture state and its allocations are the call's
+        if stream.device.index != dev:
+            raise ValueError("the stream is of %s, the tensors are on cuda:%d" % (stream.device, dev))
+        with torch.cuda.stream(stream):
+            return _run_q8(what, entry, like, workspace, None, args)
     if _get_device() != dev:
         with torch.cuda.device(dev):
-            return _run_q8(what, entry, like, workspace, stream, args)
+            return _run_q8(what, entry, like, workspace, None, args)
     call = getattr(_marshal or _marshal_module(), entry)
-    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    raw = _raw_stream(dev)
     capturing = _capturing()
     if workspace is None and not capturing:
         # the device's workspace, one for each stream other than the default one
@@ -638,8 +644,7 @@ def _run_q8(what, entry, like, workspace, stream, args):
             raise RuntimeError("the workspace cannot grow while a graph is captured: run the "
                                "call once before, or leave the workspace out")
         else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(raw, dev)):
-                buf = workspace.get(-rc)
+            buf = workspace.get(-rc)
         rc = call(*args, buf, raw)
     if rc != MSA_OK:
         raise MsaError(rc, what)

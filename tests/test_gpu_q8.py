@@ -598,6 +598,40 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, want[i]) for o in outs[i])
 
 
+def test_stream_argument():
+    """``stream=`` runs the call on that stream: its place in the order, its capture state
+    and its allocations."""
+    g = gen(44)
+    block, h, d, H, max_kv = 64, 2, 64, 8, 3000
+    c, _ = random_cache(g, batch=1, max_kv=max_kv, h=h, d=d, d_idx=32, block=block, paged=False)
+    nblk = -(-max_kv // block)
+    q = rows(g, 1, 1, H, d)
+    ids = ids_for(g, [max_kv], 1, h, nblk, block, 32)
+
+    def call(**kw):
+        return msa.msa_sparse_attn_q8(q, c.k, c.v, c.k_scale, c.v_scale, ids, block=block, **kw)
+
+    want = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out = call(stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    out.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        call(stream=side, out=out)
+        torch.cuda.current_stream().wait_stream(side)
+    assert not out.any()  # captured, not run
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_cache_larger_than_32_bit_offsets():
     """2^31 codes and more in one tensor: the last row is written, scored, attended to and
     read back."""
