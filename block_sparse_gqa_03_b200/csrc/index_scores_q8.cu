@@ -5,12 +5,14 @@
 //
 // What bounds it: L_b * d_idx bytes of HBM per sequence, half of the bf16 scan's.
 // Persistent, one CTA per SM, each an equal contiguous share of the flattened items (a
-// block of a sequence, or 64 tokens of smaller blocks); warp w takes items w, w + 12, ...  Each warp streams its own
+// block of a sequence, or 64 tokens of smaller blocks: a block of 16 at a time took 29 us
+// for 9 x 60K tokens, four of them 13.5 us); the CTA's warps take its items in turn.  Each
+// warp streams its own
 // items: it resolves 32 of them at a time (one per lane: sequence, block, page,
 // scale), its lane 0 issues the TMA loads (rows of d_idx bytes, swizzled by the row
 // size) into the warp's private ring of stages and refills a stage as soon as the
 // warp has read it.  One producer warp for all of them, as in the bf16 scan, issues an
-// 8 KB block every 250 ns at best: 61.7 us against 52.5 us for 16 x 128K tokens of 128
+// 8 KB block every 250 ns at best: 61.7 us against 52.3 us for 16 x 128K tokens of 128
 // dims (41.7 us of HBM time).
 //
 // A code row is read by ldmatrix as pairs of bytes: a lane's 32-bit register holds
@@ -40,7 +42,7 @@ struct ScanQ8Args {
   KvPages pg;
 };
 
-constexpr int kWarps = 12;  // 8: 53.4 us for the scan above, 12: 52.5, 16: 53.9
+constexpr int kWarps = 12;  // 8: 53.4 us for the scan above, 12: 52.3, 16: 53.9
 constexpr int kMaxDepth = 16;  // stages of a warp
 
 __device__ __forceinline__ int seq_blocks(const ScanQ8Args& a, int b) {

@@ -253,6 +253,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         heap_i[i * kHeapRows + hr] = 0xffffu;
       }
     }
+    if (a.scores != nullptr && a.fill_tail && ng < ng_valid) {
+      // this CTA's share of the blocks no query of the tile sees, the warp's rows one after
+      // the other so that the stores are contiguous, while the first tile is on its way
+      // (after the last tile, a row per round, they cost 6 of 61 us of the chunk below)
+      const int tail = n_all * bpt, len = max(0, a.nblk - tail);
+      const int c0 = tail + (int)((int64_t)len * sp / a.n_split);
+      const int wide = tail + (int)((int64_t)len * (sp + 1) / a.n_split) - c0;
+      const int tq = t0 + quarter * 32, rows = min(32, a.n_q - tq);
+      const int step = wide < (1 << 24) ? 32 : 1;  // rows whose elements fit 32 bits
+      for (int r0 = 0; r0 < rows; r0 += step) {
+        float* dst = a.scores + c0 +
+                     (((int64_t)b * a.n_q + tq + r0) * a.h + gp * kNG + ng) * (int64_t)a.nblk;
+        const int total = min(step, rows - r0) * wide;
+        for (int x = lane; x < total; x += 32) {
+          const int r = x / wide;
+          dst[(int64_t)r * a.h * a.nblk + (x - r * wide)] = ninf;
+        }
+      }
+    }
     for (int kt = 0; kt < n_kt && ng < ng_valid; ++kt) {
       const int buf = kt & 1;
       if (!mbar_wait_warp(b_afull + 8 * buf, (kt >> 1) & 1, a.st, 0x106u, a.wait_ns)) break;
@@ -328,18 +347,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-      }
-    }
-    if (a.scores != nullptr && a.fill_tail && ng < ng_valid) {
-      // this CTA's share of the blocks no query of the tile sees, a row of the warp at a
-      // time so that the stores are contiguous
-      const int tail = n_all * bpt, len = max(0, a.nblk - tail);
-      const int c0 = tail + (int)((int64_t)len * sp / a.n_split);
-      const int c1 = tail + (int)((int64_t)len * (sp + 1) / a.n_split);
-      for (int r = 0; r < 32 && t0 + quarter * 32 + r < a.n_q; ++r) {
-        const int64_t tr = (int64_t)b * a.n_q + t0 + quarter * 32 + r;
-        float* dst = a.scores + (tr * a.h + gp * kNG + ng) * (int64_t)a.nblk;
-        for (int beta = c0 + lane; beta < c1; beta += 32) dst[beta] = ninf;
       }
     }
     if constexpr (TOPK) {

@@ -19,9 +19,9 @@
 //  * the merge buffer's rows are padded by 16 bytes (unpadded, four lanes met on one
 //    bank at every store).
 // Bound: HBM, 2 d bytes per selected visible token and group.  16 x 128K tokens, 64
-// heads in 8 groups of 128 dims, 128 of 2048 blocks each: 52.3 us against 41.4 us of
-// HBM time (268 MB at the measured copy rate); of the rest 4 us pass before the first
-// block arrives and 4 to 6 us after the last one, in the rows' merges.
+// heads in 8 groups of 128 dims, 128 of 2048 blocks each: 50.6 us against 41.4 us of
+// HBM time (268 MB at the measured copy rate; the bf16 cache: 93 us); of the rest about
+// 4 us pass before the first block arrives, the others in the merges behind the last one.
 // A block's K scale joins the softmax scale of its scores and its V scale the fp32
 // accumulation of its product, so that neither is rounded to 16 bits.
 #include <math.h>
@@ -901,8 +901,8 @@ AttnPlan plan_attn_q8(const Shape& s) {
     const double t = fmax(0.1, 2.0 * s.d * s.block / 44000.0);
     pl.per = max(pl.per, (int)ceil(sqrt(s.topk * 0.18 / t)));
     // Whole rows where that adds at most a block per warp (2 us): a split row's partials
-    // are published and merged in 3 to 4 us.  (One sequence of 2 groups with 8 blocks:
-    // SMALLA us with split rows, SMALLB us without.)
+    // are published and merged in 3 to 4 us.  (128 rows of 16 blocks: 14.7 us
+    // with split rows, 12.1 us with whole ones.)
     const int whole = (pl.per + s.topk - 1) / s.topk * s.topk;
     if (whole - pl.per <= kStreamNC) pl.per = whole;
     pl.per = min(pl.per, kMaxList);
