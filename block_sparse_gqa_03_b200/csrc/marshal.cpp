@@ -4,6 +4,7 @@
 // A decode step makes a few calls of 4 to 50 us of GPU time each.  Read attribute by
 // attribute from Python, ten tensors cost about 9 us a call; here about 1 us.
 #include <Python.h>
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -348,6 +349,35 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
+// empty(like, lead, last, type): a new tensor of like's first `lead` sizes and, unless it
+// is negative, `last`; type 0: like's own, 1: fp32, 2: int32.  A result made with
+// Tensor.new_empty costs 2.7 us of a call whose kernel takes 5, here 1 us.
+PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    if (n != 4) refuse("wrong number of arguments");
+    const at::Tensor& like = *tensor(args[0], "like");
+    const int64_t lead = integer(args[1]), last = integer(args[2]), type = integer(args[3]);
+    if (lead < 0 || lead > like.dim()) refuse("the query has shape " + describe(like));
+    c10::SmallVector<int64_t, 5> shape(like.sizes().begin(), like.sizes().begin() + lead);
+    if (last >= 0) shape.push_back(last);
+    return THPVariable_Wrap(at::empty(
+        shape, like.options().dtype(type == 0   ? like.scalar_type()
+                                    : type == 1 ? at::kFloat
+                                                : at::kInt)));
+  } catch (const std::invalid_argument& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::OutOfMemoryError& e) {
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
 // bind(addresses of the seven library functions, in Api's order)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 7) {
@@ -377,6 +407,8 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&bind)), METH_FASTCALL,
+     nullptr},
+    {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&empty)), METH_FASTCALL,
      nullptr},
     MSA_ENTRY("append", append, 15),
     MSA_ENTRY("read", read, 16),

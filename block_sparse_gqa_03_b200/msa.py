@@ -582,7 +582,6 @@ def q8_cache(*, h, d, d_idx, block, batch=None, max_kv=None, num_pages=None, dev
                    codes(planes, rows, d_idx), ones(*scales, h), ones(*scales, h), ones(*scales))
 
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _get_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _capturing = torch._C._cuda_isCurrentStreamCapturing
@@ -657,6 +656,12 @@ def _blocks(codes, block, block_table, max_kv):
     return -(-(codes.shape[1] if block_table is None else max_kv or 0) // block)
 
 
+def _empty(like, lead, last=-1, kind=0):
+    """A new tensor of ``like``'s first ``lead`` sizes and, unless negative, ``last``; of
+    ``like``'s type (0), fp32 (1) or int32 (2)."""
+    return (_marshal or _marshal_module()).empty(like, lead, last, kind)
+
+
 def msa_append_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new=None, v_new=None,
                      k_idx_new=None, *, block, seq_lens=None, block_table=None, max_kv=None,
                      workspace: Workspace | None = None, stream=None):
@@ -681,11 +686,11 @@ def msa_read_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, *, n, token_base=
         b = k.shape[0] if block_table is None else block_table.shape[0]
         shape = (b, n) + tuple(k.shape[2:])
         if k_out is None:
-            k_out = k.new_zeros(shape, dtype=_BF16)
+            k_out = k.new_zeros(shape, dtype=torch.bfloat16)
         if v_out is None:
-            v_out = k.new_zeros(shape, dtype=_BF16)
+            v_out = k.new_zeros(shape, dtype=torch.bfloat16)
         if k_idx_out is None:
-            k_idx_out = k.new_zeros((b, n, k_idx.shape[-1]), dtype=_BF16)
+            k_idx_out = k.new_zeros((b, n, k_idx.shape[-1]), dtype=torch.bfloat16)
     if k_out.shape[1] != n:
         raise ValueError("k_out holds %d rows, not %d" % (k_out.shape[1], n))
     _run_q8("msa_read_kv_q8", "read", k, workspace, stream,
@@ -699,8 +704,7 @@ def msa_block_scores_q8(q_idx, k_idx, k_idx_scale, *, block, causal=True, seq_le
                         workspace: Workspace | None = None, stream=None):
     """msa_block_scores over the 8-bit index key: fp32 [b, n_q, h, nblk]."""
     if block_scores is None:
-        block_scores = q_idx.new_empty(
-            q_idx.shape[:3] + (_blocks(k_idx, block, block_table, max_kv),), dtype=_F32)
+        block_scores = _empty(q_idx, 3, _blocks(k_idx, block, block_table, max_kv), 1)
     _run_q8("msa_block_scores_q8", "index", q_idx, workspace, stream,
             (q_idx, k_idx, k_idx_scale, None, block_scores, causal, False, block, seq_lens,
              block_table, max_kv))
@@ -713,14 +717,12 @@ def msa_index_select_q8(q_idx, k_idx, k_idx_scale, *, block, topk, causal=True,
                         workspace: Workspace | None = None, stream=None):
     """msa_index_select over the 8-bit index key: block ids int32 [b, n_q, h, topk] (and the
     fp32 block scores if asked)."""
-    lead = q_idx.shape[:3]
     if block_ids is None:
-        block_ids = q_idx.new_empty(lead + (topk,), dtype=_I32)
+        block_ids = _empty(q_idx, 3, topk, 2)
     elif block_ids.shape[-1] != topk:
         raise ValueError("block_ids holds %d blocks, not %d" % (block_ids.shape[-1], topk))
     if return_scores and block_scores is None:
-        block_scores = q_idx.new_empty(lead + (_blocks(k_idx, block, block_table, max_kv),),
-                                       dtype=_F32)
+        block_scores = _empty(q_idx, 3, _blocks(k_idx, block, block_table, max_kv), 1)
     _run_q8("msa_index_select_q8", "index", q_idx, workspace, stream,
             (q_idx, k_idx, k_idx_scale, block_ids, block_scores, causal, force_own_block, block,
              seq_lens, block_table, max_kv))
@@ -734,9 +736,9 @@ def msa_sparse_attn_q8(q, k, v, k_scale, v_scale, block_ids, *, block, causal=Tr
     """msa_sparse_attn over the 8-bit cache: bf16 output [b, n_q, H, d] (and fp32 lse
     [b, n_q, H] if asked)."""
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q, 4)
     if return_lse and lse is None:
-        lse = q.new_empty(q.shape[:3], dtype=_F32)
+        lse = _empty(q, 3, kind=1)
     _run_q8("msa_sparse_attn_q8", "attn", q, workspace, stream,
             (q, k, v, k_scale, v_scale, block_ids, out, lse, causal, softmax_scale, block,
              seq_lens, block_table, max_kv))
@@ -750,16 +752,14 @@ def msa_forward_q8(q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, *, bloc
                    workspace: Workspace | None = None, stream=None):
     """msa_forward over the 8-bit cache; returns out, plus (ids, scores, lse) when asked,
     in that order."""
-    lead = q_idx.shape[:3]
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q, 4)
     if return_ids and block_ids is None:
-        block_ids = q.new_empty(lead + (topk,), dtype=_I32)
+        block_ids = _empty(q_idx, 3, topk, 2)
     if return_scores and block_scores is None:
-        block_scores = q.new_empty(lead + (_blocks(k_idx, block, block_table, max_kv),),
-                                   dtype=_F32)
+        block_scores = _empty(q_idx, 3, _blocks(k_idx, block, block_table, max_kv), 1)
     if return_lse and lse is None:
-        lse = q.new_empty(q.shape[:3], dtype=_F32)
+        lse = _empty(q, 3, kind=1)
     _run_q8("msa_forward_q8", "forward", q, workspace, stream,
             (q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, out, block_ids, block_scores,
              lse, topk, causal, force_own_block, softmax_scale, block, seq_lens, block_table,
