@@ -85,7 +85,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
                "-fvisibility=hidden", "-I" + inc,
                "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
                "-I" + sysconfig.get_paths()["include"], src, "-o", tmp, "-L" + lib,
-               "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+               "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)

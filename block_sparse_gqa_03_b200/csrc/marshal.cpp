@@ -4,6 +4,7 @@
 // A decode step makes a few calls of 4 to 50 us of GPU time each.  Read attribute by
 // attribute from Python, ten tensors cost about 9 us a call; here about 1 us.
 #include <Python.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -351,7 +352,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // empty(like, lead, last, type): a new tensor of like's first `lead` sizes and, unless it
 // is negative, `last`; type 0: like's own, 1: fp32, 2: int32.  A result made with
-// Tensor.new_empty costs 2.7 us of a call whose kernel takes 5, here 1 us.
+// Tensor.new_empty costs 2.8 us of a call whose kernel takes 6, here 0.75 us (at::empty: 1.2).
 PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
     if (n != 4) refuse("wrong number of arguments");
@@ -360,10 +361,9 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (lead < 0 || lead > like.dim()) refuse("the query has shape " + describe(like));
     c10::SmallVector<int64_t, 5> shape(like.sizes().begin(), like.sizes().begin() + lead);
     if (last >= 0) shape.push_back(last);
-    return THPVariable_Wrap(at::empty(
-        shape, like.options().dtype(type == 0   ? like.scalar_type()
-                                    : type == 1 ? at::kFloat
-                                                : at::kInt)));
+    const at::ScalarType t = type == 0 ? like.scalar_type() : type == 1 ? at::kFloat : at::kInt;
+    if (!like.is_cuda()) return THPVariable_Wrap(at::empty(shape, t));  // refused by the call
+    return THPVariable_Wrap(at::Tensor(at::detail::empty_cuda(shape, t, like.device(), {})));
   } catch (const std::invalid_argument& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const c10::OutOfMemoryError& e) {
