@@ -272,6 +272,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
+    // Blocks of 16 and 32 store a tile's scores four at a time: one by one, each store of a
+    // warp touches 32 sectors for 128 bytes (2048 queries over 32K in blocks of 16: 114 us,
+    // four at a time 57 us).  With the two of a block of 64 nothing is gained.
+    const bool vec = a.nblk % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scores) & 15u) == 0;
     for (int kt = 0; kt < n_kt && ng < ng_valid; ++kt) {
       const int buf = kt & 1;
       if (!mbar_wait_warp(b_afull + 8 * buf, (kt >> 1) & 1, a.st, 0x106u, a.wait_ns)) break;
@@ -307,9 +311,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (row_ok) {
         if (srow != nullptr) {
+          const int b0 = j0 / BLK;
+          if (bpt < 4 || !vec) {
 #pragma unroll
-          for (int k = 0; k < bpt; ++k)
-            if (j0 / BLK + k < a.nblk) srow[j0 / BLK + k] = bm[k];
+            for (int k = 0; k < bpt; ++k)
+              if (b0 + k < a.nblk) srow[b0 + k] = bm[k];
+          } else {
+#pragma unroll
+            for (int k = 0; k < bpt; k += 4)
+              if (b0 + k < a.nblk)
+                *reinterpret_cast<float4*>(srow + b0 + k) =
+                    make_float4(bm[k], bm[k + 1], bm[k + 2], bm[k + 3]);
+          }
         }
         if constexpr (TOPK) {
 #pragma unroll

@@ -598,6 +598,31 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, want[i]) for o in outs[i])
 
 
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("max_kv", [1024, 1000])
+def test_scores_of_small_blocks_at_any_address(block, max_kv):
+    """A prompt's scores are stored four blocks at a time where rows are 16-byte aligned:
+    the same bits elsewhere, and nothing beside them."""
+    g = gen(45)
+    c, _ = random_cache(g, batch=2, max_kv=max_kv, h=3, d=64, d_idx=64, block=block, paged=False)
+    lens = torch.tensor([max_kv, 417], dtype=torch.int32, device=DEV)
+    qi = rows(g, 2, 150, 3, 64)
+    nblk = -(-max_kv // block)
+    kw = dict(block=block, seq_lens=lens)
+    want = msa.msa_block_scores_q8(qi, c.k_idx, c.k_idx_scale, **kw)
+    _, _, key = ref_values(c, None, block, 1, max_kv)
+    ref, mag = q8_ref.scores(qi[1].double(), key, 417, block, True)
+    fin = torch.isfinite(ref)
+    assert torch.equal(torch.isneginf(want[1]), ~fin)
+    assert bool(((want[1].double() - ref).abs()[fin] <= mag[fin] * 2.0 ** -16).all())
+    for shift in (1, 2, 4):
+        buf = torch.full((want.numel() + 8,), 7.0, device=DEV)
+        part = buf[shift:shift + want.numel()].view(want.shape)
+        msa.msa_block_scores_q8(qi, c.k_idx, c.k_idx_scale, block_scores=part, **kw)
+        assert torch.equal(part, want) and part.shape[-1] == nblk
+        assert bool((buf[:shift] == 7).all() and (buf[shift + want.numel():] == 7).all())
+
+
 def test_stream_argument():
     """``stream=`` runs the call on that stream: its place in the order, its capture state
     and its allocations."""
