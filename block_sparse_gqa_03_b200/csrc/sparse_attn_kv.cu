@@ -54,6 +54,8 @@
 // Buffers: 2-4 Q tiles (released when S is computed), 2 K/V stages, and in tensor
 // memory 3-4 slots, each holding a tile's S and then its O, plus the two P
 // regions.  Every wait is bounded.
+#include <algorithm>
+
 #include "kernels.h"
 #include "q8.cuh"
 #include "sm100.cuh"
@@ -1228,9 +1230,22 @@ cudaError_t run_kv(const Shape& s, KvArgs& a, const KvPlan& p, const CUtensorMap
 
 }  // namespace
 
+// Over an 8-bit cache, few rows that read little go to the one-CTA-per-row kernel: its
+// blocks come from L2 again for every row, but nothing is listed, written and merged.
+// Rows (of 8 heads), blocks of 64 tokens of 128 dims each, KV-major and by row:
+//   1200 x 4: 34.8, 17.7 us   1200 x 8: 40.2, 25.9   4000 x 2: 42.3, 37.1
+//   4000 x 4: 54.8, 48.4      1200 x 16: 53.0, 51.2  16000 x 1: 85.2, 119.7
+// 4000 x 4 with groups of one head: 37.4, 40.5, of 16 heads: 107.5, 85.9; 620 rows of one
+// block of 64 dims: 22.5, 7.8.
+bool few_rows_q8(const Shape& s) {
+  const int64_t rows = (int64_t)s.batch * s.n_q * s.h;
+  return s.kv8 && rows <= 4096 &&
+         rows * std::min(s.topk, s.nblk) * s.block * 2 * s.d <= ((int64_t)256 << 20);
+}
+
 bool kv_attn_supported(const Shape& s) {
   // partial rows are addressed with int32
-  return s.n_q > 1 && (s.d == 64 || s.d == 128) && (s.block == 64 || s.block == 128) &&
+  return !few_rows_q8(s) && s.n_q > 1 && (s.d == 64 || s.d == 128) && (s.block == 64 || s.block == 128) &&
          plan_kv(s).max_tiles * kRows < ((int64_t)1 << 31);
 }
 

@@ -291,11 +291,18 @@ ATTN_CASES = [
     (20, 4, 2, 64, 32, 3, 120, [120, 64], False),
     (333, 20, 2, 64, 32, 6, 700, [700, 100, 333], True),    # one row per block of threads
     (400, 16, 2, 128, 16, 5, 400, [400], True),
-    (300, 6, 2, 64, 64, 4, 300, [300, 299], True),          # queries gathered by block
+    (300, 6, 2, 64, 64, 4, 300, [300, 299], True),
     (260, 32, 4, 128, 64, 6, 600, [600, 261, 100], True),
     (300, 16, 1, 128, 128, 3, 500, [500, 300], True),
     (310, 10, 2, 64, 128, 2, 310, [310, 77], False),
     (200, 48, 16, 128, 64, 3, 256, [256], True),
+    # more than 4096 rows, gathered by block
+    (540, 24, 8, 64, 64, 4, 600, [600, 541], True),
+    (520, 8, 8, 128, 128, 2, 700, [700, 300], True),         # queries before the first token
+    (4200, 6, 1, 64, 128, 2, 4200, [4200], False),
+    (1100, 64, 4, 128, 64, 5, 1100, [1100], True),
+    (700, 18, 2, 64, 64, 17, 2000, [2000, 1500, 700], True),
+    (280, 32, 16, 128, 64, 3, 320, [300], True),
     # many sequences: one CTA per row, short and long lists, groups on both sides of 8
     (1, 16, 8, 64, 64, 3, 200, [200 - i for i in range(80)], True),
     (1, 24, 8, 128, 64, 20, 1500, [1500 - 19 * i for i in range(75)], True),
@@ -345,7 +352,7 @@ def test_sparse_attn_scales_far_apart_and_peaked_rows():
     and scores large enough that single keys win."""
     g = gen(21)
     lens, block, h, d, H = [256, 250], 64, 2, 128, 8
-    c, _ = random_cache(g, batch=2, max_kv=256, h=h, d=d, d_idx=32, block=block, paged=False)
+    c, _ = random_cache(g, batch=2, max_kv=1200, h=h, d=d, d_idx=32, block=block, paged=False)
     c.k_scale.fill_(2.0 ** -7)
     c.k_scale[:, 1] = 1.0
     c.v_scale[:, 0], c.v_scale[:, 2] = 2.0 ** -40, 2.0 ** 20
@@ -353,14 +360,14 @@ def test_sparse_attn_scales_far_apart_and_peaked_rows():
     q = rows(g, 2, 1, H, d)
     ids = torch.tensor([3, 1, -1, 0], dtype=torch.int32, device=DEV).expand(2, 1, h, 4).contiguous()
     sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
-    for n in (1, 130):
+    for n in (1, 130, 1100):  # streamed, by row, by block
         qq, ii = q.expand(2, n, H, d).contiguous(), ids.expand(2, n, h, 4).contiguous()
         out, lse = msa.msa_sparse_attn_q8(qq, c.k, c.v, c.k_scale, c.v_scale, ii, block=block,
                                           seq_lens=sl, return_lse=True)
-        check_attn(c, None, qq, ii, lens, block, 256, out, lse)
+        check_attn(c, None, qq, ii, lens, block, 1200, out, lse)
 
 
-@pytest.mark.parametrize("n", [1, 70, 280])
+@pytest.mark.parametrize("n", [1, 70, 280, 480])
 def test_layouts_give_the_same_bits(n):
     """Token-major, head-major and padded caches, and pages, hold the same values."""
     g = gen(22)
@@ -431,15 +438,16 @@ def test_bad_page_is_recorded_and_reads_as_zeros():
 def test_ids_out_of_range_are_skipped_and_recorded():
     g = gen(24)
     block, h, d, H = 64, 1, 64, 4
-    for n in (1, 700):
-        c, _ = random_cache(g, batch=1, max_kv=700, h=h, d=d, d_idx=32, block=block, paged=False)
+    for n, max_kv in ((1, 700), (700, 700), (4200, 4200)):  # streamed, by row, by block
+        c, _ = random_cache(g, batch=1, max_kv=max_kv, h=h, d=d, d_idx=32, block=block, paged=False)
         q = rows(g, 1, n, H, d)
-        ids = torch.tensor([0, 11, 2, 10], dtype=torch.int32, device=DEV).expand(1, n, h, 4).contiguous()
+        ids = torch.tensor([0, -(-max_kv // block), 2, 10], dtype=torch.int32, device=DEV)
+        ids = ids.expand(1, n, h, 4).contiguous()
         ws = msa.Workspace(DEV)
         out, lse = msa.msa_sparse_attn_q8(q, c.k, c.v, c.k_scale, c.v_scale, ids, block=block,
                                           return_lse=True, workspace=ws)
         assert msa.msa_get_device_status(ws) == msa.MSA_ERR_DEVICE_ASSERT
-        check_attn(c, None, q, ids, [700], block, 700, out, lse)
+        check_attn(c, None, q, ids, [max_kv], block, max_kv, out, lse)
 
 
 # ------------------------------------------------------------- a run of them together
@@ -501,10 +509,10 @@ def test_8bit_attention_is_the_bf16_attention_of_the_read_back_cache():
                         spread=0)
     sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
     k, v, ki = msa.msa_read_kv_q8(*c, n=900, block=block, seq_lens=sl)
-    for n in (1, 400):
+    for n, topk in ((1, 4), (400, 4), (900, 6)):  # streamed, by row, by block
         q, qi = rows(g, 2, n, H, d), rows(g, 2, n, h, di)
         kw = dict(block=block, seq_lens=sl)
-        ids = msa.msa_index_select_q8(qi, c.k_idx, c.k_idx_scale, topk=4, **kw)
+        ids = msa.msa_index_select_q8(qi, c.k_idx, c.k_idx_scale, topk=topk, **kw)
         out, lse = msa.msa_sparse_attn_q8(q, c.k, c.v, c.k_scale, c.v_scale, ids, return_lse=True,
                                           **kw)
         out2, lse2 = msa.msa_sparse_attn(q, k, v, ids, return_lse=True, **kw)
