@@ -432,12 +432,13 @@ cudaError_t run_tc(const Shape& s, const uint16_t* q_idx, const uint16_t* k_idx,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   // Few query tiles (a chunk of a prompt, a short batch): the key tiles are split over
-  // CTAs up to one wave, at least 8 tiles each (every block's score depends on its own
+  // CTAs up to one wave, at least 2 tiles each (every block's score depends on its own
   // tile alone; the streaming top-k needs them all in one CTA).  2048 queries, 4 groups
-  // of 64 dims, 32K keys: 32 CTAs took 181 us, 4 shares each 46 us.
+  // of 64 dims, 32K keys: 32 CTAs took 181 us, 4 shares each 46 us.  1043 queries, 3 groups
+  // of 128 dims, 1780 keys, with the widening: 25 us with at least 8 tiles each, 14 with 2.
   const int64_t ctas = (int64_t)s.batch * a.n_gpairs * a.n_mtiles;
   const int tiles = (s.max_kv + kKT - 1) / kKT;
-  a.n_split = TOPK ? 1 : (int)max((int64_t)1, min(num_sms() / ctas, (int64_t)tiles / 8));
+  a.n_split = TOPK ? 1 : (int)max((int64_t)1, min(num_sms() / ctas, (int64_t)tiles / 2));
   const unsigned grid = (unsigned)(ctas * a.n_split);
   return launch_pdl(index_score_tc_kernel<DI, BLK, TOPK>, dim3(grid), dim3(kTcThreads), smem,
                     stream, tmq, tmk, a);
