@@ -608,22 +608,27 @@ def _marshal_module():
 _marshal = None
 
 
-def _run_q8(what, entry, like, workspace, stream, args):
-    """One library call through the marshalling extension, on ``like``'s device.  The
-    extension checks every tensor, and answers with the library's status or, before it
-    launches anything, with minus the workspace bytes it needs."""
+def _on_stream(call, like, kw):
+    """``call(**kw)`` with ``kw["stream"]`` as the current stream: what the call allocates,
+    fills and launches, and its capture state, are that stream's.  ``like``: a tensor of the
+    call's device."""
+    stream, dev = kw.pop("stream"), like.get_device()
+    if stream.device.index != dev:
+        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, like.device))
+    with torch.cuda.stream(stream):
+        return call(**kw)
+
+
+def _run_q8(what, entry, like, workspace, args):
+    """One library call through the marshalling extension, on ``like``'s device and its
+    current stream.  The extension checks every tensor, and answers with the library's
+    status or, before it launches anything, with minus the workspace bytes it needs."""
     dev = like.get_device()
     if dev < 0:
         raise ValueError("the 8-bit cache calls need CUDA tensors")
-    if stream is not None:
-        # made current: its capture state and its allocations are the call's
-        if stream.device.index != dev:
-            raise ValueError("the stream is of %s, the tensors are on cuda:%d" % (stream.device, dev))
-        with torch.cuda.stream(stream):
-            return _run_q8(what, entry, like, workspace, None, args)
     if _get_device() != dev:
         with torch.cuda.device(dev):
-            return _run_q8(what, entry, like, workspace, None, args)
+            return _run_q8(what, entry, like, workspace, args)
     call = getattr(_marshal or _marshal_module(), entry)
     raw = _raw_stream(dev)
     capturing = _capturing()
@@ -669,9 +674,11 @@ def msa_append_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new=None, v_n
     k_idx_new [b, n_new, d_idx] (dense) are quantised into positions L_b - n_new + t, and
     the scales of the blocks they fall into are set (see ``include/msa.h``).  Any of the
     new tensors may be None (its part of the cache is not written)."""
+    if stream is not None:
+        return _on_stream(msa_append_kv_q8, k, locals())
     if k_new is None and v_new is None and k_idx_new is None:
         raise ValueError("no new rows")
-    _run_q8("msa_append_kv_q8", "append", k, workspace, stream,
+    _run_q8("msa_append_kv_q8", "append", k, workspace,
             (k, v, k_idx, k_scale, v_scale, k_idx_scale, k_new, v_new, k_idx_new, block, seq_lens,
              block_table, max_kv))
 
@@ -682,6 +689,8 @@ def msa_read_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, *, n, token_base=
     """Rows [token_base, token_base + n) of every sequence of an 8-bit cache as bf16:
     (k [b, n, h, d], v, k_idx [b, n, d_idx]).  Rows at positions past a sequence's end are
     left as they were in the given outputs, and are zeros in those made here."""
+    if stream is not None:
+        return _on_stream(msa_read_kv_q8, k, locals())
     if k_out is None or v_out is None or k_idx_out is None:
         b = k.shape[0] if block_table is None else block_table.shape[0]
         shape = (b, n) + tuple(k.shape[2:])
@@ -693,7 +702,7 @@ def msa_read_kv_q8(k, v, k_idx, k_scale, v_scale, k_idx_scale, *, n, token_base=
             k_idx_out = k.new_zeros((b, n, k_idx.shape[-1]), dtype=torch.bfloat16)
     if k_out.shape[1] != n:
         raise ValueError("k_out holds %d rows, not %d" % (k_out.shape[1], n))
-    _run_q8("msa_read_kv_q8", "read", k, workspace, stream,
+    _run_q8("msa_read_kv_q8", "read", k, workspace,
             (k, v, k_idx, k_scale, v_scale, k_idx_scale, k_out, v_out, k_idx_out, token_base,
              block, seq_lens, block_table, max_kv))
     return k_out, v_out, k_idx_out
@@ -703,9 +712,11 @@ def msa_block_scores_q8(q_idx, k_idx, k_idx_scale, *, block, causal=True, seq_le
                         block_scores=None, block_table=None, max_kv=None,
                         workspace: Workspace | None = None, stream=None):
     """msa_block_scores over the 8-bit index key: fp32 [b, n_q, h, nblk]."""
+    if stream is not None:
+        return _on_stream(msa_block_scores_q8, q_idx, locals())
     if block_scores is None:
         block_scores = _empty(q_idx, 3, _blocks(k_idx, block, block_table, max_kv), 1)
-    _run_q8("msa_block_scores_q8", "index", q_idx, workspace, stream,
+    _run_q8("msa_block_scores_q8", "index", q_idx, workspace,
             (q_idx, k_idx, k_idx_scale, None, block_scores, causal, False, block, seq_lens,
              block_table, max_kv))
     return block_scores
@@ -717,13 +728,15 @@ def msa_index_select_q8(q_idx, k_idx, k_idx_scale, *, block, topk, causal=True,
                         workspace: Workspace | None = None, stream=None):
     """msa_index_select over the 8-bit index key: block ids int32 [b, n_q, h, topk] (and the
     fp32 block scores if asked)."""
+    if stream is not None:
+        return _on_stream(msa_index_select_q8, q_idx, locals())
     if block_ids is None:
         block_ids = _empty(q_idx, 3, topk, 2)
     elif block_ids.shape[-1] != topk:
         raise ValueError("block_ids holds %d blocks, not %d" % (block_ids.shape[-1], topk))
     if return_scores and block_scores is None:
         block_scores = _empty(q_idx, 3, _blocks(k_idx, block, block_table, max_kv), 1)
-    _run_q8("msa_index_select_q8", "index", q_idx, workspace, stream,
+    _run_q8("msa_index_select_q8", "index", q_idx, workspace,
             (q_idx, k_idx, k_idx_scale, block_ids, block_scores, causal, force_own_block, block,
              seq_lens, block_table, max_kv))
     return (block_ids, block_scores) if return_scores else block_ids
@@ -735,11 +748,13 @@ def msa_sparse_attn_q8(q, k, v, k_scale, v_scale, block_ids, *, block, causal=Tr
                        stream=None):
     """msa_sparse_attn over the 8-bit cache: bf16 output [b, n_q, H, d] (and fp32 lse
     [b, n_q, H] if asked)."""
+    if stream is not None:
+        return _on_stream(msa_sparse_attn_q8, q, locals())
     if out is None:
         out = _empty(q, 4)
     if return_lse and lse is None:
         lse = _empty(q, 3, kind=1)
-    _run_q8("msa_sparse_attn_q8", "attn", q, workspace, stream,
+    _run_q8("msa_sparse_attn_q8", "attn", q, workspace,
             (q, k, v, k_scale, v_scale, block_ids, out, lse, causal, softmax_scale, block,
              seq_lens, block_table, max_kv))
     return (out, lse) if return_lse else out
@@ -752,6 +767,8 @@ def msa_forward_q8(q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, *, bloc
                    workspace: Workspace | None = None, stream=None):
     """msa_forward over the 8-bit cache; returns out, plus (ids, scores, lse) when asked,
     in that order."""
+    if stream is not None:
+        return _on_stream(msa_forward_q8, q, locals())
     if out is None:
         out = _empty(q, 4)
     if return_ids and block_ids is None:
@@ -760,7 +777,7 @@ def msa_forward_q8(q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, *, bloc
         block_scores = _empty(q_idx, 3, _blocks(k_idx, block, block_table, max_kv), 1)
     if return_lse and lse is None:
         lse = _empty(q, 3, kind=1)
-    _run_q8("msa_forward_q8", "forward", q, workspace, stream,
+    _run_q8("msa_forward_q8", "forward", q, workspace,
             (q, k, v, q_idx, k_idx, k_scale, v_scale, k_idx_scale, out, block_ids, block_scores,
              lse, topk, causal, force_own_block, softmax_scale, block, seq_lens, block_table,
              max_kv))
