@@ -262,6 +262,17 @@ def _check(rc: int, what: str):
         raise MsaError(rc, what)
 
 
+def _on_stream(call, like, kw):
+    """``call(**kw)`` with ``kw["stream"]`` as the current stream: what the call allocates,
+    fills and launches, its workspace's first clearing and its capture state are that
+    stream's.  ``like``: a tensor of the call's device, or None."""
+    stream = kw.pop("stream")
+    if like is not None and stream.device.index != like.get_device():
+        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, like.device))
+    with torch.cuda.stream(stream):
+        return call(**kw)
+
+
 def _kv_extent(k, block_table, max_kv):
     """max_kv and the page count: the tensor's token axis, or for a page pool the
     caller's max_kv and the pool's first axis."""
@@ -278,6 +289,8 @@ def msa_index_select(q_idx, k_idx, *, block, topk, causal=True, force_own_block=
                      stream=None):
     """Stage 1: block ids int32 [b, n_q, h, topk] (and fp32 block scores if asked).
     With ``block_table``, ``k_idx`` is a page pool [num_pages, block, d_idx]."""
+    if stream is not None:
+        return _on_stream(msa_index_select, q_idx, locals())
     b, n_q, h, d_idx = q_idx.shape
     max_kv, num_pages = _kv_extent(k_idx, block_table, max_kv)
     nblk = (max_kv + block - 1) // block
@@ -296,7 +309,7 @@ def msa_index_select(q_idx, k_idx, *, block, topk, causal=True, force_own_block=
     ws = _workspace(workspace, dev).get(need)
     _check(load_library().msa_index_select(ctypes.byref(p), _ptr(q_idx), _ptr(k_idx),
                                            _ptr(block_ids), _ptr(block_scores), ws.data_ptr(),
-                                           ws.numel(), _stream(stream)), "msa_index_select")
+                                           ws.numel(), _stream()), "msa_index_select")
     return (block_ids, block_scores) if return_scores else block_ids
 
 
@@ -305,6 +318,8 @@ def msa_sparse_attn(q, k, v, block_ids, *, block, causal=True, seq_lens=None, so
                     workspace: Workspace | None = None, stream=None):
     """Stage 2: bf16 output [b, n_q, H, d] (and fp32 lse [b, n_q, H] if asked).
     With ``block_table``, ``k`` and ``v`` are page pools [num_pages, block, h, d]."""
+    if stream is not None:
+        return _on_stream(msa_sparse_attn, q, locals())
     b, n_q, H, d = q.shape
     h = k.shape[2]
     max_kv, num_pages = _kv_extent(k, block_table, max_kv)
@@ -322,7 +337,7 @@ def msa_sparse_attn(q, k, v, block_ids, *, block, causal=True, seq_lens=None, so
     ws = _workspace(workspace, q.device).get(need)
     _check(load_library().msa_sparse_attn(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v),
                                           _ptr(block_ids), _ptr(out), _ptr(lse), ws.data_ptr(),
-                                          ws.numel(), _stream(stream)), "msa_sparse_attn")
+                                          ws.numel(), _stream()), "msa_sparse_attn")
     return (out, lse) if return_lse else out
 
 
@@ -331,6 +346,8 @@ def msa_sparse_attn_noalloc(q, k, v, block_ids, *, block, causal=True, seq_lens=
     """Stage 2 without a workspace (the library's fixed device scratch holds the
     split-KV partials); for callers that cannot allocate device memory.  ``out``
     (and ``lse``, if wanted) should be preallocated by such callers."""
+    if stream is not None:
+        return _on_stream(msa_sparse_attn_noalloc, q, locals())
     b, n_q, H, d = q.shape
     max_kv, h = k.shape[1], k.shape[2]
     if out is None:
@@ -340,7 +357,7 @@ def msa_sparse_attn_noalloc(q, k, v, block_ids, *, block, causal=True, seq_lens=
                     seq_lens=seq_lens, q=q, k=k, v=v, out=out)
     _check(load_library().msa_sparse_attn_noalloc(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v),
                                                   _ptr(block_ids), _ptr(out), _ptr(lse),
-                                                  _stream(stream)), "msa_sparse_attn_noalloc")
+                                                  _stream()), "msa_sparse_attn_noalloc")
     return out
 
 
@@ -352,6 +369,8 @@ def msa_append_kv(k, v, k_idx, k_new=None, v_new=None, k_idx_new=None, *, block,
     [b, max_kv, h, d] and k_idx [b, max_kv, d_idx] (or of the page pools, with
     ``block_table``).  Any of the new tensors may be None, and then its cache too
     (``k`` or ``v`` must be given for the shapes)."""
+    if stream is not None:
+        return _on_stream(msa_append_kv, k if k is not None else v, locals())
     ref = next(t for t in (k_new, v_new, k_idx_new) if t is not None)
     b, n_new = ref.shape[0], ref.shape[1]
     kv = k if k is not None else v
@@ -370,7 +389,7 @@ def msa_append_kv(k, v, k_idx, k_new=None, v_new=None, k_idx_new=None, *, block,
     ws = _workspace(workspace, kv.device).get(need)
     _check(load_library().msa_append_kv(ctypes.byref(p), _ptr(k_new), _ptr(v_new),
                                         _ptr(k_idx_new), _ptr(k), _ptr(v), _ptr(k_idx),
-                                        ws.data_ptr(), ws.numel(), _stream(stream)),
+                                        ws.data_ptr(), ws.numel(), _stream()),
            "msa_append_kv")
 
 
@@ -381,6 +400,8 @@ def msa_forward(q, k, v, q_idx, k_idx, *, block, topk, causal=True, force_own_bl
                 params: Params | None = None):
     """Both stages; returns out, plus (ids, scores, lse) when asked, in that order.
     With ``block_table``, ``k``, ``v`` and ``k_idx`` are page pools."""
+    if stream is not None:
+        return _on_stream(msa_forward, q, locals())
     b, n_q, H, d = q.shape
     h = k.shape[2]
     max_kv, num_pages = _kv_extent(k, block_table, max_kv)
@@ -406,7 +427,7 @@ def msa_forward(q, k, v, q_idx, k_idx, *, block, topk, causal=True, force_own_bl
     ws = _workspace(workspace, dev).get(need)
     _check(load_library().msa_forward(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(q_idx),
                                       _ptr(k_idx), _ptr(out), _ptr(block_ids), _ptr(block_scores),
-                                      _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream)),
+                                      _ptr(lse), ws.data_ptr(), ws.numel(), _stream()),
            "msa_forward")
     res = [out]
     if return_ids:
@@ -422,6 +443,8 @@ def msa_block_scores(q_idx, k_idx, *, block, causal=True, seq_lens=None, block_s
                      block_table=None, max_kv=None, workspace: Workspace | None = None,
                      stream=None):
     """Stage 1, first half: fp32 block scores [b, n_q, h, nblk] (-inf past the frontier)."""
+    if stream is not None:
+        return _on_stream(msa_block_scores, q_idx, locals())
     b, n_q, h, d_idx = q_idx.shape
     max_kv, num_pages = _kv_extent(k_idx, block_table, max_kv)
     nblk = (max_kv + block - 1) // block
@@ -433,7 +456,7 @@ def msa_block_scores(q_idx, k_idx, *, block, causal=True, seq_lens=None, block_s
     ws = _workspace(workspace, q_idx.device).get(msa_workspace_size(p, MSA_OP_BLOCK_SCORES))
     _check(load_library().msa_block_scores(ctypes.byref(p), _ptr(q_idx), _ptr(k_idx),
                                            _ptr(block_scores), ws.data_ptr(), ws.numel(),
-                                           _stream(stream)), "msa_block_scores")
+                                           _stream()), "msa_block_scores")
     return block_scores
 
 
@@ -441,6 +464,8 @@ def msa_index_candidates(q_idx, k_idx, *, block, topk, causal=True, force_own_bl
                          seq_lens=None, block_ids=None, kept_scores=None, block_table=None,
                          max_kv=None, workspace: Workspace | None = None, stream=None):
     """msa_index_select plus the kept blocks' scores: (ids, scores), both [b, n_q, h, topk]."""
+    if stream is not None:
+        return _on_stream(msa_index_candidates, q_idx, locals())
     b, n_q, h, d_idx = q_idx.shape
     max_kv, num_pages = _kv_extent(k_idx, block_table, max_kv)
     p = make_params(batch=b, n_q=n_q, max_kv=max_kv, H=h, h=h, d=64, d_idx=d_idx, block=block,
@@ -458,7 +483,7 @@ def msa_index_candidates(q_idx, k_idx, *, block, topk, causal=True, force_own_bl
     ws = _workspace(workspace, dev).get(need)
     _check(load_library().msa_index_candidates(ctypes.byref(p), _ptr(q_idx), _ptr(k_idx),
                                                _ptr(block_ids), _ptr(kept_scores), ws.data_ptr(),
-                                               ws.numel(), _stream(stream)),
+                                               ws.numel(), _stream()),
            "msa_index_candidates")
     return block_ids, kept_scores
 
@@ -470,6 +495,8 @@ def msa_select_candidates(cand_scores, cand_ids, *, max_kv, block, topk, shard_b
     """Global top-k from gathered candidate lists [nlists, b, n_q, h, len] (list r's ids
     local to the shard starting at block r * shard_blocks); returns the global ids and/or
     the ids local to the shard [block_base, block_base + nblk_local)."""
+    if stream is not None:
+        return _on_stream(msa_select_candidates, cand_ids, locals())
     nlists, b, n_q, h, llen = cand_ids.shape
     if not (cand_ids.is_contiguous() and cand_scores.is_contiguous()):
         raise ValueError("candidate lists must be dense")
@@ -486,13 +513,15 @@ def msa_select_candidates(cand_scores, cand_ids, *, max_kv, block, topk, shard_b
         ctypes.byref(p), int(nlists), int(llen), int(shard_blocks), _ptr(cand_scores),
         _ptr(cand_ids), int(block_base), int(nblk_local),
         _ptr(block_ids if want_global else None), _ptr(local_ids if want_local else None),
-        ws.data_ptr(), ws.numel(), _stream(stream)), "msa_select_candidates")
+        ws.data_ptr(), ws.numel(), _stream()), "msa_select_candidates")
     return block_ids, local_ids
 
 
 def msa_merge_partials(part_out, part_lse, *, out=None, lse=None, h=None, stream=None):
     """LSE merge of part_out bf16 [P, b, n_q, H, d] with part_lse fp32 [P, b, n_q, H].
     ``h`` (the KV heads) only has to make a valid head grouping of H."""
+    if stream is not None:
+        return _on_stream(msa_merge_partials, part_out, locals())
     P, b, n_q, H, d = part_out.shape
     if not (part_out.is_contiguous() and part_lse.is_contiguous()):
         raise ValueError("partials must be dense")
@@ -504,13 +533,15 @@ def msa_merge_partials(part_out, part_lse, *, out=None, lse=None, h=None, stream
                     topk=1, out=out)
     _check(load_library().msa_merge_partials(ctypes.byref(p), int(P), _ptr(part_out),
                                              _ptr(part_lse), _ptr(out), _ptr(lse),
-                                             _stream(stream)), "msa_merge_partials")
+                                             _stream()), "msa_merge_partials")
     return out
 
 
 def msa_shard_lengths(seq_lens, *, batch, max_kv, token_base, token_count, out=None,
                       workspace: Workspace | None = None, stream=None, device=None):
     """Per-sequence token counts inside the shard [token_base, token_base + token_count)."""
+    if stream is not None:
+        return _on_stream(msa_shard_lengths, seq_lens, locals())
     dev = seq_lens.device if seq_lens is not None else torch.device(device or "cuda")
     if out is None:
         out = torch.empty((batch,), dtype=torch.int32, device=dev)
@@ -519,7 +550,7 @@ def msa_shard_lengths(seq_lens, *, batch, max_kv, token_base, token_count, out=N
     ws = _workspace(workspace, dev).get(msa_workspace_size(p, MSA_OP_SHARD_LENGTHS))
     _check(load_library().msa_shard_lengths(ctypes.byref(p), int(token_base), int(token_count),
                                             _ptr(out), ws.data_ptr(), ws.numel(),
-                                            _stream(stream)), "msa_shard_lengths")
+                                            _stream()), "msa_shard_lengths")
     return out
 
 
@@ -529,6 +560,8 @@ def msa_index_topk(q_idx, k_idx, *, block, topk, causal=True, force_own_block=Fa
                    stream=None):
     """Stage 1 for prefill in one kernel (the top-k kept in the index GEMM's epilogue):
     the ids of msa_index_select, and the block scores only if asked."""
+    if stream is not None:
+        return _on_stream(msa_index_topk, q_idx, locals())
     b, n_q, h, d_idx = q_idx.shape
     max_kv, num_pages = _kv_extent(k_idx, block_table, max_kv)
     nblk = (max_kv + block - 1) // block
@@ -544,7 +577,7 @@ def msa_index_topk(q_idx, k_idx, *, block, topk, causal=True, force_own_block=Fa
     ws = _workspace(workspace, dev).get(msa_workspace_size(p, MSA_OP_INDEX_TOPK))
     _check(load_library().msa_index_topk(ctypes.byref(p), _ptr(q_idx), _ptr(k_idx),
                                          _ptr(block_ids), _ptr(block_scores), ws.data_ptr(),
-                                         ws.numel(), _stream(stream)), "msa_index_topk")
+                                         ws.numel(), _stream()), "msa_index_topk")
     return (block_ids, block_scores) if return_scores else block_ids
 
 
@@ -606,17 +639,6 @@ def _marshal_module():
 
 
 _marshal = None
-
-
-def _on_stream(call, like, kw):
-    """``call(**kw)`` with ``kw["stream"]`` as the current stream: what the call allocates,
-    fills and launches, and its capture state, are that stream's.  ``like``: a tensor of the
-    call's device."""
-    stream, dev = kw.pop("stream"), like.get_device()
-    if stream.device.index != dev:
-        raise ValueError("the stream is of %s, the tensors are on %s" % (stream.device, like.device))
-    with torch.cuda.stream(stream):
-        return call(**kw)
 
 
 def _run_q8(what, entry, like, workspace, args):

@@ -92,6 +92,80 @@ def test_a_stream_of_another_device_is_refused(name, streams):
     assert not log
 
 
+def bf16_calls():
+    """The bf16 calls with everything left to them, by name: (call, results they make)."""
+    def z(*shape, dtype=BF16):
+        return torch.zeros(shape, dtype=dtype)
+
+    q, qi = z(1, 1, 4, 64), z(1, 1, 2, 32)
+    k, ki, ids = z(1, 64, 2, 64), z(1, 64, 32), z(1, 1, 2, 1, dtype=torch.int32)
+    sel = dict(block=16, topk=2)
+    return {
+        "index_select": (lambda **kw: msa.msa_index_select(qi, ki, return_scores=True, **sel, **kw), 2),
+        "index_topk": (lambda **kw: msa.msa_index_topk(qi, ki, return_scores=True, **sel, **kw), 2),
+        "block_scores": (lambda **kw: msa.msa_block_scores(qi, ki, block=16, **kw), 1),
+        "index_candidates": (lambda **kw: msa.msa_index_candidates(qi, ki, **sel, **kw), 2),
+        "select_candidates": (lambda **kw: msa.msa_select_candidates(
+            z(1, 1, 1, 2, 2, dtype=torch.float32), z(1, 1, 1, 2, 2, dtype=torch.int32), max_kv=64,
+            want_local=True, **sel, **kw), 2),
+        "sparse_attn": (lambda **kw: msa.msa_sparse_attn(q, k, k, ids, block=16, return_lse=True,
+                                                         **kw), 2),
+        "sparse_attn_noalloc": (lambda **kw: msa.msa_sparse_attn_noalloc(q, k, k, ids, block=16,
+                                                                         **kw), 1),
+        "append_kv": (lambda **kw: msa.msa_append_kv(k, k, ki, k[:, :1], None, None, block=16,
+                                                     **kw), 0),
+        "append_kv_values": (lambda **kw: msa.msa_append_kv(None, k, ki, None, k[:, :1], None,
+                                                            block=16, **kw), 0),
+        "merge_partials": (lambda **kw: msa.msa_merge_partials(
+            z(2, 1, 1, 4, 64), z(2, 1, 1, 4, dtype=torch.float32), **kw), 1),
+        "shard_lengths": (lambda **kw: msa.msa_shard_lengths(
+            z(1, dtype=torch.int32), batch=1, max_kv=64, token_base=0, token_count=32, **kw), 1),
+        "shard_lengths_none": (lambda **kw: msa.msa_shard_lengths(
+            None, batch=1, max_kv=64, token_base=0, token_count=32, device="cpu", **kw), 1),
+        "forward": (lambda **kw: msa.msa_forward(q, k, k, qi, ki, return_ids=True,
+                                                 return_scores=True, return_lse=True, **sel, **kw), 4),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(bf16_calls()))
+def test_results_of_the_bf16_calls_are_made_on_their_stream(name, streams, monkeypatch):
+    side, log = streams
+    call, made = bf16_calls()[name]
+    buffer = torch.zeros(1 << 16, dtype=torch.uint8)
+    empty, empty_like = torch.empty, torch.empty_like
+
+    class Library:
+        def __getattr__(self, entry):
+            def launch(*args):
+                log.append((entry, Recording.current))
+                return 0
+            return launch
+
+    class Space:
+        def get(self, nbytes):
+            log.append(("workspace", Recording.current))
+            return buffer
+
+    monkeypatch.setattr(msa, "load_library", lambda: Library())
+    monkeypatch.setattr(msa, "msa_workspace_size", lambda *a: 4096)
+    monkeypatch.setattr(msa, "_workspace", lambda *a: Space())
+    monkeypatch.setattr(msa, "_stream", lambda stream=None: stream.cuda_stream if stream else 0)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (log.append(("empty", Recording.current)),
+                                                         empty(*a, **k))[1])
+    monkeypatch.setattr(torch, "empty_like", lambda *a, **k: (
+        log.append(("empty", Recording.current)), empty_like(*a, **k))[1])
+    call(stream=side)
+    assert [n for n, _ in log].count("empty") == made and log[-1][0].startswith("msa_")
+    assert all(s is side for _, s in log), log
+    log.clear()
+    call()
+    assert all(s is None for _, s in log) and log[-1][0].startswith("msa_")
+    if name != "shard_lengths_none":
+        side.device.index = 3
+        with pytest.raises(ValueError, match="stream"):
+            call(stream=side)
+
+
 # ------------------------------------------------------------------------ on a GPU
 def queue_work(ms=10):
     """Milliseconds of work on the current stream."""
@@ -141,6 +215,27 @@ def test_results_of_a_side_stream_do_not_take_memory_of_the_busy_current_one():
     where = {t.data_ptr() for t in held}
     del held
     got = msa.msa_forward_q8(q, *cache, stream=side, **kw)
+    assert not where & {t.data_ptr() for t in got}
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_bf16_results_of_a_side_stream_while_the_current_one_is_busy():
+    """With a workspace of its own that this call makes and clears: the clearing is ordered
+    before the call, not behind the work of the current stream."""
+    c, q, qi = filled_cache()
+    k, v, ki = msa.msa_read_kv_q8(*c, n=1000, block=64)
+    kw = dict(block=64, topk=8, return_ids=True, return_scores=True, return_lse=True)
+    want = msa.msa_forward(q, k, v, qi, ki, **kw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    queue_work()
+    held = [torch.full_like(t, 3) for t in want for _ in range(4)]  # queued behind the work
+    where = {t.data_ptr() for t in held}
+    del held
+    got = msa.msa_forward(q, k, v, qi, ki, workspace=msa.Workspace("cuda"), stream=side, **kw)
     assert not where & {t.data_ptr() for t in got}
     torch.cuda.synchronize()
     for a, b in zip(got, want):
