@@ -655,8 +655,9 @@ def _run_q8(what, entry, like, workspace, args):
     raw = _raw_stream(dev)
     capturing = _capturing()
     if workspace is None and not capturing:
-        # the device's workspace, one for each stream other than the default one
-        key = (dev, raw) if raw else dev
+        # one for each stream, none of them shared with the bf16 calls, whose one for the
+        # device may be in use on any stream
+        key = (dev, raw)
         workspace = _default_ws.get(key)
         if workspace is None:
             workspace = _default_ws[key] = Workspace(torch.device("cuda", dev))
