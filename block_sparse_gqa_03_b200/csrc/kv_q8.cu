@@ -111,6 +111,9 @@ __global__ void __launch_bounds__(kThreads) append_kv_q8_kernel(Q8Args a) {
   const Unit w = unit_of(a, u);
   if (w.src == nullptr) return;
   const int L = kv_length(a.seq_lens, b, a.max_kv, a.st);
+  // a length out of range (recorded by kv_length) has no place for the rows: at the end of
+  // the cache they would replace the last ones
+  if (a.seq_lens != nullptr && a.seq_lens[b] != L) return;
   const int start = L - a.n;  // position of the first new row
   if (start < 0 && slot == 0 && threadIdx.x == 0)
     record_error(a.st, kErrDeviceAssert, 0x30000u | (uint32_t)b);

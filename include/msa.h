@@ -367,9 +367,10 @@ MSA_API msa_status_t msa_sparse_attn_noalloc(const msa_params_t* params, const m
  * elements: infinities become +-448 s', NaN stays NaN.  The first row of a block
  * starts it afresh (whatever a recycled page held is ignored); rows behind the new
  * ones are left as they were.  A page may receive rows of one sequence only.
- * A position < 0, a page id outside the pool, or a scale of a block with older rows
- * that is no power of two in range is recorded as MSA_ERR_DEVICE_ASSERT, and the
- * rows it concerns are not written.
+ * A sequence length outside [0, max_kv], a position < 0, a page id outside the pool,
+ * or a scale of a block with older rows that is no power of two in range is recorded
+ * as MSA_ERR_DEVICE_ASSERT, and the rows it concerns (of a length: the sequence's) are
+ * not written.
  * Any of the three new tensors may be NULL, but not all (its cache and scale
  * pointers may then be NULL).  Workspace: the status region. */
 MSA_API msa_status_t msa_append_kv_q8(const msa_params_t* params, const msa_bf16_t* k_new,
