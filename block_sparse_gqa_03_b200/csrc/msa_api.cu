@@ -632,7 +632,7 @@ msa_status_t msa_read_kv_q8(const msa_params_t* params, const msa_e4m3_t* k, con
   Shape s;
   msa_status_t rc = make_shape(params, &s);
   if (rc != MSA_OK) return rc;
-  if (token_base < 0 || token_base + s.n_q > s.max_kv || (!k_out && !v_out && !k_idx_out))
+  if (token_base < 0 || token_base > s.max_kv - s.n_q || (!k_out && !v_out && !k_idx_out))
     return MSA_ERR_INVALID_ARG;
   if ((k_out && (!aligned16(k_out) || !good_codes(k, k_scale, s.k_s, s.d))) ||
       (v_out && (!aligned16(v_out) || !good_codes(v, v_scale, s.v_s, s.d))) ||
