@@ -40,6 +40,7 @@ struct ScanArgs {
   int fill_tail;
   DeviceStatus* st;
   KvPages pg;
+  const float* scale;  // index_scan_kernel: per (sequence, block), or nullptr
 };
 
 constexpr int kScanWarps = 8;
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kScanWarps * 32) index_scan_kernel(ScanArgs a)
   for (int beta = wid; beta < F; beta += nw) {
     float cm[NT][2];
     block_max<DI, NT>(a, kidx_block(a, b, beta, q), L, beta, r, bq, lim, cm);
+    const float sc = a.scale != nullptr ? __ldg(a.scale + (int64_t)b * a.nblk + beta) : 1.f;
     if (r == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kScanWarps * 32) index_scan_kernel(ScanArgs a)
           const int c = nt * 8 + 2 * q + e;
           const int t = t0 + c / a.h, g = c % a.h;
           if (c < ncols && t < a.n_q)
-            a.scores[(((int64_t)b * a.n_q + t) * a.h + g) * a.nblk + beta] = cm[nt][e];
+            a.scores[(((int64_t)b * a.n_q + t) * a.h + g) * a.nblk + beta] = cm[nt][e] * sc;
         }
     }
   }
@@ -587,6 +589,7 @@ cudaError_t launch_index_scores(const Shape& s, const uint16_t* q_idx, const uin
   a.scores = scores;
   a.fill_tail = fill_tail ? 1 : 0;
   a.st = st;
+  a.scale = s.kis;
   // Columns per warp: all h groups of one query in decode; in prefill a tile of
   // queries whose columns fill four 8-wide MMA tiles.
   int nt;

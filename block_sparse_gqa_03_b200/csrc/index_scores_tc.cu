@@ -50,6 +50,7 @@ struct TcArgs {
   int n_mtiles, n_gpairs, n_split, stages;
   float* scores;
   int fill_tail;
+  const float* scale;  // SCALED: per (sequence, block)
   DeviceStatus* st;
   uint64_t wait_ns;
   KvPages pg;  // table == nullptr: contiguous K_idx
@@ -80,7 +81,9 @@ __device__ __forceinline__ void bitonic_sort(uint32_t (&v)[N]) {
       }
 }
 
-template <int DI, int BLK, bool TOPK>
+// SCALED: the key is in units of a scale per block, which is positive and so moves out
+// of the maximum.
+template <int DI, int BLK, bool TOPK, bool SCALED>
 __global__ void __launch_bounds__(kTcThreads, 1)
     index_score_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                           const __grid_constant__ CUtensorMap tmk, TcArgs a) {
@@ -276,8 +279,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // warp touches 32 sectors for 128 bytes (2048 queries over 32K in blocks of 16: 114 us,
     // four at a time 57 us).  With the two of a block of 64 nothing is gained.
     const bool vec = a.nblk % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scores) & 15u) == 0;
+    float held = 1.f;  // SCALED: the scale of block `lane` of the next 32
     for (int kt = 0; kt < n_kt && ng < ng_valid; ++kt) {
       const int buf = kt & 1;
+      if (SCALED && (kt * bpt) % 32 == 0)
+        held = __ldg(a.scale + (int64_t)b * a.nblk + min((kt0 + kt) * bpt + lane, a.nblk - 1));
       if (!mbar_wait_warp(b_afull + 8 * buf, (kt >> 1) & 1, a.st, 0x106u, a.wait_ns)) break;
       tc::fence_after_sync();
       const int j0 = (kt0 + kt) * kKT;
@@ -290,7 +296,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_aempty + 8 * buf);
-      float bm[bpt];
+      float bm[bpt], sc[bpt];
+#pragma unroll
+      for (int k = 0; k < bpt; ++k)
+        sc[k] = SCALED ? __shfl_sync(0xffffffffu, held, (kt * bpt + k) & 31) : 1.f;
       if (vis >= kKT) {
 #pragma unroll
         for (int k = 0; k < bpt; ++k) {
@@ -301,6 +310,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             m1 = fmax3(m1, v[k * BLK + i + 2], v[k * BLK + i + 3]);
           }
           bm[k] = fmaxf(m0, m1);
+          if constexpr (SCALED) bm[k] *= sc[k];
         }
       } else {
 #pragma unroll
@@ -308,6 +318,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int col = 0; col < kKT; ++col)
           bm[col / BLK] = fmaxf(bm[col / BLK], col < vis ? v[col] : ninf);
+        // (a block without a visible key may have no scale: past the sequence none is written)
+#pragma unroll
+        for (int k = 0; k < bpt; ++k)
+          if (SCALED && bm[k] != ninf) bm[k] *= sc[k];
       }
       if (row_ok) {
         if (srow != nullptr) {
@@ -388,7 +402,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <int DI, int BLK, bool TOPK>
+template <int DI, int BLK, bool TOPK, bool SCALED = false>
 cudaError_t run_tc(const Shape& s, const uint16_t* q_idx, const uint16_t* k_idx, TcArgs& a,
                    cudaStream_t stream) {
   EncodeTiledFn enc = encode_fn();
@@ -428,7 +442,7 @@ cudaError_t run_tc(const Shape& s, const uint16_t* q_idx, const uint16_t* k_idx,
   };
   while (a.stages > 2 && bytes(a.stages) > (size_t)max_smem_optin()) --a.stages;
   const size_t smem = bytes(a.stages);
-  cudaError_t err = cudaFuncSetAttribute(index_score_tc_kernel<DI, BLK, TOPK>,
+  cudaError_t err = cudaFuncSetAttribute(index_score_tc_kernel<DI, BLK, TOPK, SCALED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   // Few query tiles (a chunk of a prompt, a short batch): the key tiles are split over
@@ -440,7 +454,7 @@ cudaError_t run_tc(const Shape& s, const uint16_t* q_idx, const uint16_t* k_idx,
   const int tiles = (s.max_kv + kKT - 1) / kKT;
   a.n_split = TOPK ? 1 : (int)max((int64_t)1, min(num_sms() / ctas, (int64_t)tiles / 2));
   const unsigned grid = (unsigned)(ctas * a.n_split);
-  return launch_pdl(index_score_tc_kernel<DI, BLK, TOPK>, dim3(grid), dim3(kTcThreads), smem,
+  return launch_pdl(index_score_tc_kernel<DI, BLK, TOPK, SCALED>, dim3(grid), dim3(kTcThreads), smem,
                     stream, tmq, tmk, a);
 }
 
@@ -466,6 +480,7 @@ cudaError_t launch_index_scores_tc(const Shape& s, const uint16_t* q_idx, const 
   a.n_gpairs = (s.h + kNG - 1) / kNG;
   a.scores = scores;
   a.fill_tail = fill_tail ? 1 : 0;
+  a.scale = s.kis;
   a.st = st;
   a.wait_ns = 4000000000ull;
   a.pg = s.pages;
@@ -473,7 +488,9 @@ cudaError_t launch_index_scores_tc(const Shape& s, const uint16_t* q_idx, const 
   a.topk = s.topk;
   a.force_own = s.force_own;
 #define MSA_TC_CASE(DI_, BLK_) \
-  if (s.d_idx == DI_ && s.block == BLK_) return run_tc<DI_, BLK_, false>(s, q_idx, k_idx, a, stream);
+  if (s.d_idx == DI_ && s.block == BLK_)                                       \
+    return a.scale ? run_tc<DI_, BLK_, false, true>(s, q_idx, k_idx, a, stream) \
+                   : run_tc<DI_, BLK_, false>(s, q_idx, k_idx, a, stream);
   MSA_TC_CASE(128, 16)
   MSA_TC_CASE(128, 32)
   MSA_TC_CASE(128, 64)
@@ -508,6 +525,7 @@ cudaError_t launch_index_topk_tc(const Shape& s, const uint16_t* q_idx, const ui
   a.n_gpairs = (s.h + kNG - 1) / kNG;
   a.scores = scores;
   a.fill_tail = 1;
+  a.scale = nullptr;
   a.st = st;
   a.wait_ns = 4000000000ull;
   a.pg = s.pages;

@@ -21,6 +21,9 @@ struct Shape {
   // [batch, nblk, h] or [num_pages, h]
   bool kv8;
   const float *ks, *vs;
+  // index key in units of a scale per block, dense [batch, nblk]: the block maxima of the
+  // score kernels for n_q > 1 are multiplied by it (nullptr: no scales)
+  const float* kis;
 };
 
 // The tensors of an 8-bit cache: e4m3 codes with the shape's strides, and fp32
@@ -92,10 +95,11 @@ cudaError_t launch_append_kv_q8(const Shape& s, const uint16_t* k_new, const uin
                                 cudaStream_t stream);
 
 // Rows [base, base + n) of every sequence of an 8-bit cache (those below its length)
-// as bf16, dense [batch, n, h, d] / [batch, n, d_idx].
+// as bf16, dense [batch, n, h, d] / [batch, n, d_idx].  With `block_scales` ([batch,
+// nblk], base 0) the index key comes out as codes, and the scales of its blocks there.
 cudaError_t launch_read_kv_q8(const Shape& s, const Q8Cache& c, int64_t base, int64_t n,
                               uint16_t* k_out, uint16_t* v_out, uint16_t* ki_out, DeviceStatus* st,
-                              cudaStream_t stream);
+                              cudaStream_t stream, float* block_scales = nullptr);
 
 // Stage 1a/1b over an 8-bit index key, one query per sequence (index_scores_q8.cu).
 cudaError_t launch_index_scan_q8(const Shape& s, const uint16_t* q_idx, const uint8_t* k_idx,

@@ -42,6 +42,7 @@ struct Q8Args {
   int per_seq;      // write: block slots of a sequence; read: token groups
   int64_t base;     // read: first position
   int group;        // read: tokens per CTA
+  float* block_scales;  // read: the index key comes out as codes, its scales here
 };
 
 constexpr int kThreads = 128;
@@ -209,6 +210,8 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
     scale_at = plane;
   }
   const bool bad = plane < 0;  // recorded by kv_page; the rows read as zeros
+  if (a.block_scales != nullptr && threadIdx.x == 0 && p0 == (int64_t)beta * a.block)
+    a.block_scales[(int64_t)b * a.nblk + beta] = bad ? 1.f : a.kis[scale_at];
   const int rows = (int)(p1 - p0);
   const int64_t out0 = (int64_t)b * a.n + (p0 - a.base);
   // K and V: piece = (head, row, 16 codes), a head's rows together
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
         if (!bad) {
           x[i] = ld_stream_u4(codes + plane * st[0] + (row0 + r) * st[1] +
                               (heads > 1 ? g * st[2] : 0) + c * 16);
-          s[i] = __ldg(scales + scale_at * heads + g);
+          if (scales != nullptr) s[i] = __ldg(scales + scale_at * heads + g);
         }
         o[i] = out + ((out0 + r) * heads + g) * d + c * 16;
       }
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
   };
   plane_of(a.k, a.k_s, a.ks, a.h, a.d, a.k_out);
   plane_of(a.v, a.v_s, a.vs, a.h, a.d, a.v_out);
-  plane_of(a.ki, a.ki_s, a.kis, 1, a.d_idx, a.ki_out);
+  plane_of(a.ki, a.ki_s, a.block_scales == nullptr ? a.kis : nullptr, 1, a.d_idx, a.ki_out);
 }
 
 Q8Args base_args(const Shape& s, const Q8Cache& c, DeviceStatus* st) {
@@ -308,13 +311,14 @@ cudaError_t launch_append_kv_q8(const Shape& s, const uint16_t* k_new, const uin
 
 cudaError_t launch_read_kv_q8(const Shape& s, const Q8Cache& c, int64_t base, int64_t n,
                               uint16_t* k_out, uint16_t* v_out, uint16_t* ki_out, DeviceStatus* st,
-                              cudaStream_t stream) {
+                              cudaStream_t stream, float* block_scales) {
   Q8Args a = base_args(s, c, st);
   a.n = (int)n;
   a.k_out = k_out;
   a.v_out = v_out;
   a.ki_out = ki_out;
   a.base = base;
+  a.block_scales = block_scales;
   a.group = s.block < 32 ? s.block : 32;
   a.per_seq = (int)((base + n - 1) / a.group - base / a.group + 1);
   const int64_t grid = (int64_t)s.batch * a.per_seq;

@@ -132,7 +132,7 @@ msa_status_t make_shape(const msa_params_t* p, Shape* s) {
   s->pages.stride = p->table_stride;
   s->pages.pages = p->num_pages;
   s->kv8 = false;
-  s->ks = s->vs = nullptr;
+  s->ks = s->vs = s->kis = nullptr;
   if (p->block_table != nullptr) {
     // one page per block; page coordinates are int32 in the tensor maps
     if ((reinterpret_cast<uintptr_t>(p->block_table) & 3u) != 0 || p->table_stride < nblk ||
@@ -207,10 +207,15 @@ msa_status_t check_attn_args_q8(const Shape& s, const void* q, const void* k, co
 bool q8_op(msa_op_t op) { return op >= MSA_OP_APPEND_KV_Q8 && op <= MSA_OP_FORWARD_Q8; }
 
 // Prefill scores over an 8-bit index key run the bf16 index kernels on a widened
-// copy of the key, which costs 5 bytes per key element against the 2 d_idx n_q h
-// operations that each element enters.
+// copy of the codes, which costs 5 bytes per key element against the 2 d_idx n_q h
+// operations that each element enters, and multiply the block maxima by the scales,
+// which lie, dense, behind it: every code is a bf16 number, so nothing is rounded.
 size_t wide_idx_bytes(const Shape& s) {
-  return s.n_q > 1 ? (size_t)s.batch * s.max_kv * s.d_idx * 2 : 0;
+  return s.n_q > 1 ? align_up((size_t)s.batch * s.max_kv * s.d_idx * 2) : 0;
+}
+
+size_t wide_scale_bytes(const Shape& s) {
+  return s.n_q > 1 ? (size_t)s.batch * s.nblk * sizeof(float) : 0;
 }
 
 size_t scores_bytes(const Shape& s) {
@@ -235,7 +240,7 @@ Layout layout(const Shape& s, msa_op_t op) {
   l.part_bytes = 0;
   if (op == MSA_OP_BLOCK_SCORES_Q8 || op == MSA_OP_INDEX_SELECT_Q8 || op == MSA_OP_FORWARD_Q8) {
     l.wide_off = off;
-    off = align_up(off + wide_idx_bytes(s));
+    off = align_up(off + wide_idx_bytes(s) + wide_scale_bytes(s));
   }
   if (op == MSA_OP_INDEX_SELECT || op == MSA_OP_INDEX_CANDIDATES || op == MSA_OP_FORWARD ||
       op == MSA_OP_INDEX_SELECT_Q8 || op == MSA_OP_FORWARD_Q8) {
@@ -577,9 +582,12 @@ cudaError_t run_scores_q8(const Shape& s, const msa_bf16_t* q_idx, const uint8_t
   msa::Q8Cache c = {};
   c.ki = const_cast<uint8_t*>(k_idx);
   c.kis = const_cast<float*>(k_idx_scale);
-  const cudaError_t e = msa::launch_read_kv_q8(s, c, 0, s.max_kv, nullptr, nullptr, wide, st, stream);
+  float* scales = reinterpret_cast<float*>(at(ws, l.wide_off + wide_idx_bytes(s)));
+  const cudaError_t e = msa::launch_read_kv_q8(s, c, 0, s.max_kv, nullptr, nullptr, wide, st,
+                                               stream, scales);
   if (e != cudaSuccess) return e;
   Shape w = s;  // the widened key is dense, one row per token
+  w.kis = scales;
   w.pages.table = nullptr;
   w.ki_s[0] = (int64_t)s.max_kv * s.d_idx;
   w.ki_s[1] = s.d_idx;

@@ -355,7 +355,7 @@ MSA_API msa_status_t msa_sparse_attn_noalloc(const msa_params_t* params, const m
  * Scales.  msa_append_kv_q8 makes powers of two from 2^-100 to 2^120, and where a
  * block already holds rows it requires one there.  The readers take any positive
  * finite scale; for one that is not a power of two, code * scale is rounded to bf16
- * by msa_read_kv_q8 and, with n_q > 1, in the index key of the score calls. */
+ * by msa_read_kv_q8 (the scores and the attention multiply by it in fp32). */
 
 /* Decode-step or prompt write into the 8-bit cache: the rows of msa_append_kv,
  * quantised.  For every (block, head) that receives rows, with x those rows:
@@ -394,7 +394,7 @@ MSA_API msa_status_t msa_read_kv_q8(const msa_params_t* params, const msa_e4m3_t
 
 /* msa_block_scores over the 8-bit index key: S[beta] = k_idx_scale * max over the
  * visible tokens of <q_idx, code>, fp32 sums.  With n_q > 1 the workspace also holds
- * a bf16 copy of the index key (msa_workspace_size(params, MSA_OP_BLOCK_SCORES_Q8)). */
+ * the codes of the index key in bf16 (msa_workspace_size(params, MSA_OP_BLOCK_SCORES_Q8)). */
 MSA_API msa_status_t msa_block_scores_q8(const msa_params_t* params, const msa_bf16_t* q_idx,
                                          const msa_e4m3_t* k_idx, const float* k_idx_scale,
                                          float* block_scores, void* workspace,
