@@ -210,12 +210,29 @@ bool q8_op(msa_op_t op) { return op >= MSA_OP_APPEND_KV_Q8 && op <= MSA_OP_FORWA
 // copy of the codes, which costs 5 bytes per key element against the 2 d_idx n_q h
 // operations that each element enters, and multiply the block maxima by the scales,
 // which lie, dense, behind it: every code is a bf16 number, so nothing is rounded.
+//
+// The copy is sized by capacity (the lengths are on the device): as many sequences at a
+// time as 1 GiB holds, so that 64 sequences of up to 1M tokens of 128 dims in pages, however
+// short they are, take 1 GiB of workspace and not 17.
+constexpr size_t kWideBudget = size_t(1) << 30;
+
+int wide_sequences(const Shape& s) {
+  const size_t one = (size_t)s.max_kv * s.d_idx * 2;
+  const size_t fit = kWideBudget / one;
+  return fit < 1 ? 1 : (fit < (size_t)s.batch ? (int)fit : s.batch);
+}
+
 size_t wide_idx_bytes(const Shape& s) {
-  return s.n_q > 1 ? align_up((size_t)s.batch * s.max_kv * s.d_idx * 2) : 0;
+  return s.n_q > 1 ? align_up((size_t)wide_sequences(s) * s.max_kv * s.d_idx * 2) : 0;
 }
 
 size_t wide_scale_bytes(const Shape& s) {
-  return s.n_q > 1 ? (size_t)s.batch * s.nblk * sizeof(float) : 0;
+  return s.n_q > 1 ? (size_t)wide_sequences(s) * s.nblk * sizeof(float) : 0;
+}
+
+int score_launches_q8(const Shape& s) {
+  const int w = wide_sequences(s);
+  return s.n_q > 1 ? 2 * ((s.batch + w - 1) / w) : 1;
 }
 
 size_t scores_bytes(const Shape& s) {
@@ -543,12 +560,12 @@ int msa_launch_count(const msa_params_t* params, msa_op_t op) {
     case MSA_OP_INDEX_TOPK: return 1;
     case MSA_OP_APPEND_KV_Q8: return 1;
     case MSA_OP_READ_KV_Q8: return 1;
-    case MSA_OP_BLOCK_SCORES_Q8: return s.n_q > 1 ? 2 : 1;
-    case MSA_OP_INDEX_SELECT_Q8: return s.n_q > 1 ? 3 : 2;
+    case MSA_OP_BLOCK_SCORES_Q8: return score_launches_q8(s);
+    case MSA_OP_INDEX_SELECT_Q8: return score_launches_q8(s) + 1;
     case MSA_OP_SPARSE_ATTN_Q8: s.kv8 = true; return msa::attn_launches(s);
     case MSA_OP_FORWARD_Q8:
       s.kv8 = true;
-      return (s.n_q > 1 ? 3 : 2) + msa::attn_launches(s);
+      return score_launches_q8(s) + 1 + msa::attn_launches(s);
   }
   return -1;
 }
@@ -579,19 +596,30 @@ cudaError_t run_scores_q8(const Shape& s, const msa_bf16_t* q_idx, const uint8_t
   if (s.n_q == 1)
     return msa::launch_index_scan_q8(s, q_idx, k_idx, k_idx_scale, scores, fill_tail, st, stream);
   uint16_t* wide = reinterpret_cast<uint16_t*>(at(ws, l.wide_off));
-  msa::Q8Cache c = {};
-  c.ki = const_cast<uint8_t*>(k_idx);
-  c.kis = const_cast<float*>(k_idx_scale);
   float* scales = reinterpret_cast<float*>(at(ws, l.wide_off + wide_idx_bytes(s)));
-  const cudaError_t e = msa::launch_read_kv_q8(s, c, 0, s.max_kv, nullptr, nullptr, wide, st,
-                                               stream, scales);
-  if (e != cudaSuccess) return e;
-  Shape w = s;  // the widened key is dense, one row per token
-  w.kis = scales;
-  w.pages.table = nullptr;
-  w.ki_s[0] = (int64_t)s.max_kv * s.d_idx;
-  w.ki_s[1] = s.d_idx;
-  return run_scores(w, q_idx, wide, scores, fill_tail, st, stream);
+  const int step = wide_sequences(s);
+  for (int b = 0; b < s.batch; b += step) {
+    // sequences [b, b + step): the same problem from b on
+    Shape p = s;
+    p.batch = s.batch - b < step ? s.batch - b : step;
+    if (s.seq_lens != nullptr) p.seq_lens = s.seq_lens + b;
+    const bool paged = s.pages.table != nullptr;
+    if (paged) p.pages.table = s.pages.table + (int64_t)b * s.pages.stride;
+    msa::Q8Cache c = {};
+    c.ki = const_cast<uint8_t*>(k_idx) + (paged ? 0 : (int64_t)b * s.ki_s[0]);
+    c.kis = const_cast<float*>(k_idx_scale) + (paged ? 0 : (int64_t)b * s.nblk);
+    cudaError_t e = msa::launch_read_kv_q8(p, c, 0, s.max_kv, nullptr, nullptr, wide, st, stream,
+                                           scales);
+    if (e != cudaSuccess) return e;
+    p.kis = scales;  // the widened key is dense, one row per token
+    p.pages.table = nullptr;
+    p.ki_s[0] = (int64_t)s.max_kv * s.d_idx;
+    p.ki_s[1] = s.d_idx;
+    e = run_scores(p, q_idx + (int64_t)b * s.qi_s[0], wide,
+                   scores + (int64_t)b * s.n_q * s.h * s.nblk, fill_tail, st, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 msa_status_t run_select_q8(const Shape& s, const msa_bf16_t* q_idx, const uint8_t* k_idx,

@@ -394,7 +394,8 @@ MSA_API msa_status_t msa_read_kv_q8(const msa_params_t* params, const msa_e4m3_t
 
 /* msa_block_scores over the 8-bit index key: S[beta] = k_idx_scale * max over the
  * visible tokens of <q_idx, code>, fp32 sums.  With n_q > 1 the workspace also holds
- * the codes of the index key in bf16 (msa_workspace_size(params, MSA_OP_BLOCK_SCORES_Q8)). */
+ * the codes of the index key in bf16, of as many sequences at a time as 1 GiB holds
+ * (msa_workspace_size(params, MSA_OP_BLOCK_SCORES_Q8)). */
 MSA_API msa_status_t msa_block_scores_q8(const msa_params_t* params, const msa_bf16_t* q_idx,
                                          const msa_e4m3_t* k_idx, const float* k_idx_scale,
                                          float* block_scores, void* workspace,

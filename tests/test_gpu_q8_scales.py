@@ -91,3 +91,53 @@ def test_a_prompt_and_a_step_rank_the_blocks_alike(d_idx):
         assert torch.equal(one[0, 0, g_], best) and torch.equal(many[0, -1, g_], best)
     # the same sums of exact products up to their order
     assert bool(((s_many[0, -1] - s_one[0, 0]).abs() <= s_one[0, 0].abs() * 2.0 ** -14).all())
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_scores_in_several_passes(paged):
+    """Sequences of 1M tokens of capacity: the keys of four are widened at a time, six give two
+    passes.  The same bits as one sequence at a time, and as the definition."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    batch, max_kv, block, h, di, n = 6, 1 << 20, 64, 2, 128, 3
+    nblk = max_kv // block
+    lens = [5000, 1, 70, max_kv if not paged else 9000, 0, 333]
+    if paged:  # pages for the rows there are, and none behind them
+        used = [-(-x // block) for x in lens]
+        c, _ = free_cache(g, batch=1, max_kv=sum(used) * block, h=1, d=64, d_idx=di, block=block,
+                          paged=True)
+        table = torch.full((batch, nblk), -7, dtype=torch.int32, device=DEV)
+        ids = torch.randperm(sum(used), device=DEV, generator=g).int()
+        for b, k in enumerate(used):
+            table[b, :k], ids = ids[:k], ids[k:]
+        key, scale = c.k_idx, c.k_idx_scale
+    else:
+        table = None
+        key = torch.randint(0, 120, (batch, max_kv, di), device=DEV, generator=g, dtype=torch.uint8)
+        scale = torch.rand((batch, nblk), device=DEV, generator=g) + 0.5
+    q = torch.randn((batch, n, h, di), device=DEV, generator=g).to(torch.bfloat16)
+    ws = msa.Workspace(DEV)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    kw = dict(block=block, max_kv=max_kv, workspace=ws, topk=4, return_scores=True)
+    ids, got = msa.msa_index_select_q8(q, key, scale, seq_lens=sl, block_table=table, **kw)
+    assert msa.msa_get_device_status(ws) == msa.MSA_OK
+    assert ws.buf.numel() < (1 << 30) + (1 << 24)
+    for b, L in enumerate(lens):
+        part = slice(b, b + 1)
+        one_ids, one = msa.msa_index_select_q8(
+            q[part], key if paged else key[part], scale if paged else scale[part],
+            seq_lens=sl[part], block_table=None if table is None else table[part], **kw)
+        assert torch.equal(one, got[part]) and torch.equal(one_ids, ids[part])
+        m = min(L, 5000)
+        if paged:
+            page = table[b, :-(-L // block)].long()
+            val = q8_ref.decode(u8(key)[page]) * scale[page].double()[:, None, None]
+            val = val.flatten(0, 1)[:m]
+        else:
+            val = q8_ref.decode(key[b, :m]) * scale[b].double().repeat_interleave(block)[:m, None]
+        if m == L and L > 0:
+            want, mag = q8_ref.scores(q[b].double(), val, L, block)
+            x, fin = got[b, :, :, :want.shape[-1]].double(), torch.isfinite(want)
+            assert torch.equal(torch.isneginf(x), ~fin)
+            assert bool(((x - want).abs()[fin] <= mag[fin] * (2.0 ** -16 + 2.0 ** -22)).all())
+        assert bool(torch.isneginf(got[b, :, :, -(-L // block):]).all())
+    assert msa.msa_get_device_status(ws) == msa.MSA_OK
