@@ -3,7 +3,7 @@
 ``python -m block_sparse_gqa_03_b200.build`` (or ``__graft_entry__.build()``)
 runs nvcc once per source for sm_100a and links a shared library next to this
 file.  The library exports only the C ABI of ``include/msa.h``.  The binding's
-marshalling extension ``_marshal.so`` is compiled next to it.
+marshalling extension ``_marshal.<torch and Python version>.so`` is compiled next to it.
 """
 
 from __future__ import annotations
@@ -12,12 +12,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmsa.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")  # Python extension: argument checks of the q8 calls
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["msa_api.cu", "index_scores.cu", "index_scores_tc.cu", "topk.cu", "sparse_attn.cu",
            "sparse_attn_kv.cu", "append_kv.cu", "shard.cu", "kv_q8.cu", "index_scores_q8.cu",
@@ -70,27 +70,43 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
-def build_marshal(force: bool = False, verbose: bool = False) -> str:
-    """Compiles the marshalling extension against this interpreter's and torch's headers."""
-    import sysconfig
-
+def marshal_path() -> str:
+    """The marshalling extension (argument checks of the 8-bit calls).  It is bound to the
+    C++ ABI of the torch and the Python it was compiled for, which its name holds: after a
+    change of either the old file is not found, instead of being loaded."""
     import torch
 
-    src = os.path.join(CSRC, "marshal.cpp")
-    if force or _stale(MARSHAL, [src, os.path.join(ROOT, "include", "msa.h")]):
-        inc = os.path.join(os.path.dirname(torch.__file__), "include")
-        lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-        tmp = MARSHAL + ".tmp%d" % os.getpid()
-        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-               "-fvisibility=hidden", "-I" + inc,
-               "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
-               "-I" + sysconfig.get_paths()["include"], src, "-o", tmp, "-L" + lib,
-               "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
-        os.replace(tmp, MARSHAL)
-    return MARSHAL
+    return os.path.join(HERE, "_marshal.torch%s%s" % (torch.__version__,
+                                                      sysconfig.get_config_var("EXT_SUFFIX")))
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str | None:
+    """Compiles the marshalling extension against this interpreter's and torch's headers.
+    None where either lacks them: the C library and the bf16 calls do without."""
+    import torch
+
+    out, src = marshal_path(), os.path.join(CSRC, "marshal.cpp")
+    if not (force or _stale(out, [src, os.path.join(ROOT, "include", "msa.h")])):
+        return out
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    python = sysconfig.get_paths()["include"]
+    for header in (os.path.join(python, "Python.h"), os.path.join(inc, "torch", "csrc", "autograd",
+                                                                 "python_variable.h")):
+        if not os.path.exists(header):
+            print("no %s: the 8-bit cache's Python calls are not built" % header, file=sys.stderr)
+            return None
+    tmp = out + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
+           "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"), "-I" + python,
+           src, "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath," + lib]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, out)
+    return out
 
 
 if __name__ == "__main__":

@@ -20,9 +20,11 @@ from typing import NamedTuple
 
 import torch
 
+from .build import marshal_path
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmsa.so")
-MARSHAL_PATH = os.path.join(_HERE, "_marshal.so")
+MARSHAL_PATH = marshal_path()
 STATUS_BYTES = 4096  # the workspace's status region (status word, decode merge counters)
 
 MSA_OK = 0
@@ -625,8 +627,9 @@ def _marshal_module():
     global _marshal
     lib = load_library()
     if not os.path.exists(MARSHAL_PATH):
-        raise RuntimeError("_marshal.so is not built (run __graft_entry__.build() or "
-                           "python -m block_sparse_gqa_03_b200.build)")
+        raise RuntimeError("%s is not built for this torch and Python (run __graft_entry__.build() "
+                           "or python -m block_sparse_gqa_03_b200.build)"
+                           % os.path.basename(MARSHAL_PATH))
     spec = importlib.util.spec_from_file_location("block_sparse_gqa_03_b200._marshal",
                                                   MARSHAL_PATH)
     module = importlib.util.module_from_spec(spec)
