@@ -203,7 +203,12 @@ def make_params(*, batch, n_q, max_kv, H, h, d, d_idx, block, topk, causal=True,
 
 class Workspace:
     """A device buffer for the library's workspace, grown on demand.  Calls that share
-    one must be ordered on one stream."""
+    one must be ordered on one stream.
+
+    Device-side errors (a bad page, id or length) are recorded in the workspace of the call,
+    so msa_get_device_status reads those of calls that were given one.  An 8-bit call that is
+    captured without one takes a buffer from the graph's pool, and what its replays record
+    there cannot be read: run the call once with a Workspace, and capture it with that."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
