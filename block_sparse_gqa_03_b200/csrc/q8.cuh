@@ -2,10 +2,12 @@
 // tokens, KV head), value = code * scale.
 //
 // The scales that the cache write makes are powers of two.  e4m3 is a floating
-// format, so a power of two costs no precision against a free scale; x / scale is
+// format, so above 2^-6 of the scale a power of two costs no precision against a free
+// scale (below, on e4m3's fixed grid, up to one bit against max |x| / 448); x / scale is
 // exact in fp32 (no rounding next to a code border depends on how the division is
 // done); a larger scale keeps every code that stays normal exact; and code * scale
-// is a bf16 number.
+// is a bf16 number (but for codes of 256 and more at a scale of 2^120, which rows above
+// 3.3e38 have: they read back as infinity).
 //
 // The tensor-core products of the decode kernels run on f16 operands: every e4m3 value
 // is an f16 value, and the hardware widens two codes per instruction.  (The e4m3 product

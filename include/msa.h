@@ -353,7 +353,8 @@ MSA_API msa_status_t msa_sparse_attn_noalloc(const msa_params_t* params, const m
  * what it means above, and queries, new rows and outputs stay bf16.
  *
  * Scales.  msa_append_kv_q8 makes powers of two from 2^-100 to 2^120, and where a
- * block already holds rows it requires one there.  The readers take any positive
+ * block already holds rows it requires one there.  (Rows above 3.3e38 in magnitude come
+ * out as codes of 256 at 2^120, i.e. as infinities.)  The readers take any positive
  * finite scale; for one that is not a power of two, code * scale is rounded to bf16
  * by msa_read_kv_q8 (the scores and the attention multiply by it in fp32). */
 
