@@ -23,6 +23,7 @@
 
 #include "kernels.h"
 #include "q8.cuh"
+#include "sm100.cuh"
 
 namespace msa {
 namespace {
@@ -52,15 +53,6 @@ __device__ __forceinline__ int seq_blocks(const ScanQ8Args& a, int b) {
 __device__ __forceinline__ int seq_items(const ScanQ8Args& a, int b) {
   const int per = a.block < 64 ? 64 : a.block;
   return (kv_length(a.seq_lens, b, a.max_kv, a.st) + per - 1) / per;
-}
-
-__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                              int tok, int plane) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(tok), "r"(plane), "r"(bar)
-      : "memory");
 }
 
 // NB: blocks of an item (block 16: 4, 32: 2, else 1).
@@ -175,11 +167,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       const uint32_t dst = ring + (uint32_t)is * a.stage_bytes, bar = bars + 8 * is;
       mbar_arrive_expect_tx(bar, a.stage_bytes);
       if (!paged) {
-        tma_load_rows(dst, &tmk, bar, ej * a.block + sub * 64, bj);
+        tma_load_3d(dst, &tmk, bar, 0, ej * a.block + sub * 64, bj);
       } else {
 #pragma unroll
         for (int k = 0; k < NB; ++k)
-          tma_load_rows(dst + (uint32_t)(k * (64 / NB) * DI), &tmk, bar, sub * 64, pj[k]);
+          tma_load_3d(dst + (uint32_t)(k * (64 / NB) * DI), &tmk, bar, 0, sub * 64, pj[k]);
       }
     }
     __syncwarp();

@@ -1237,7 +1237,7 @@ cudaError_t run_kv(const Shape& s, KvArgs& a, const KvPlan& p, const CUtensorMap
 //   4000 x 4: 54.8, 48.4      1200 x 16: 53.0, 51.2  16000 x 1: 85.2, 119.7
 // 4000 x 4 with groups of one head: 37.4, 40.5, of 16 heads: 107.5, 85.9; 620 rows of one
 // block of 64 dims: 22.5, 7.8.
-bool few_rows_q8(const Shape& s) {
+static bool few_rows_q8(const Shape& s) {
   const int64_t rows = (int64_t)s.batch * s.n_q * s.h;
   return s.kv8 && rows <= 4096 &&
          rows * std::min(s.topk, s.nblk) * s.block * 2 * s.d <= ((int64_t)256 << 20);
