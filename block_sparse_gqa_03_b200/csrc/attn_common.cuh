@@ -68,14 +68,14 @@ __device__ __forceinline__ RowGeo row_geo(const AttnArgs& a, int64_t row) {
 // Merge of NC warp states for tile row `row`, dims [dim, dim + 4) (dim a
 // multiple of 4): normalised output and natural-log LSE (-inf and 0 when no key
 // was seen).  The warps' weights are computed once for the four dims.  LD: floats from
-// one O row to the next.
-template <int D, int NC, int LD = D>
+// one O row to the next.  NANS: a NaN maximum of a warp makes the row NaN.
+template <int D, int NC, int LD = D, bool NANS = false>
 __device__ __forceinline__ void merge_warps4(const float* mo, const float* mm, const float* ml,
                                              int gr, int row, int dim, float4& val, float& lsev) {
   const float ninf = neg_inf();
   float M = ninf;
 #pragma unroll
-  for (int w = 0; w < NC; ++w) M = fmaxf(M, mm[w * 16 + row]);
+  for (int w = 0; w < NC; ++w) M = NANS ? fmax_nan(M, mm[w * 16 + row]) : fmaxf(M, mm[w * 16 + row]);
   val = make_float4(0.f, 0.f, 0.f, 0.f);
   lsev = ninf;
   if (M == ninf) return;

@@ -305,6 +305,18 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
+// Maxima that are NaN when an operand is (fmaxf and fmax3 leave a NaN out).
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Packed two-wide fp32 arithmetic of sm_100 (one instruction for two lanes of
 // work, round to nearest even as the scalar forms): d = a * b + c, d = a + b and
 // d = a * b element-wise on (lo, hi) pairs.
@@ -365,6 +377,9 @@ __device__ __forceinline__ uint32_t pack_bf16_int(float lo, float hi) {
 
 __device__ __forceinline__ float warp_max_xor(float v, int mask) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, mask));
+}
+__device__ __forceinline__ float warp_max_xor_nan(float v, int mask) {
+  return fmax_nan(v, __shfl_xor_sync(0xffffffffu, v, mask));
 }
 
 }  // namespace msa

@@ -365,6 +365,13 @@ __device__ __forceinline__ float2 unpack_part(uint32_t x) {
   return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
+// The maximum of two partials' log-sum-exps; of an 8-bit cache NaN when either is, so that
+// a NaN partial makes the merged row NaN.
+template <bool Q8>
+__device__ __forceinline__ float part_max(float a, float b) {
+  return Q8 ? fmax_nan(a, b) : fmaxf(a, b);
+}
+
 template <int D, int BLK, bool Q8>
 __global__ void __launch_bounds__(kKvThreads, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -784,8 +791,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         }
         tc::tmem_wait_st();
         const float l = (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        rstat[(idx & 3) * kRows + row] =
-            make_float2(l > 0.f ? 1.f / l : 0.f, (ms != ninf && l > 0.f) ? (msafe + log2f(l)) * kLn2 : ninf);
+        // (l is 0 where the row sees no key; a NaN score makes it NaN, which the 8-bit form
+        // hands on to the output)
+        if constexpr (Q8)
+          rstat[(idx & 3) * kRows + row] =
+              make_float2(l != 0.f ? 1.f / l : 0.f, l != 0.f ? (msafe + log2f(l)) * kLn2 : ninf);
+        else
+          rstat[(idx & 3) * kRows + row] =
+              make_float2(l > 0.f ? 1.f / l : 0.f, (ms != ninf && l > 0.f) ? (msafe + log2f(l)) * kLn2 : ninf);
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
@@ -926,13 +939,14 @@ __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int 
     if (s < a.topk) {
       const float* l = a.part_lse + (p0 + s) * G;
 #pragma unroll
-      for (int h = 0; h < GC; ++h) M[h] = fmaxf(M[h], __ldg(l + h));
+      for (int h = 0; h < GC; ++h) M[h] = part_max<Q8>(M[h], __ldg(l + h));
     }
   }
 #pragma unroll
   for (int h = 0; h < GC; ++h)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M[h] = fmaxf(M[h], __shfl_xor_sync(0xffffffffu, M[h], o));
+    for (int o = 16; o > 0; o >>= 1)
+      M[h] = part_max<Q8>(M[h], __shfl_xor_sync(0xffffffffu, M[h], o));
   // this lane's heads hi = i * RPI + rl
   float Mp[MI * RPI];
 #pragma unroll
@@ -1006,7 +1020,8 @@ __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int 
                    pack_bf16(acc[i][4] * inv, acc[i][5] * inv),
                    pack_bf16(acc[i][6] * inv, acc[i][7] * inv));
     if (c == 0 && a.lse)
-      a.lse[(int64_t)bt * a.H + hq] = Mi[i] != ninf && den[i] > 0.f ? Mi[i] + __logf(den[i]) : ninf;
+      a.lse[(int64_t)bt * a.H + hq] =
+          Mi[i] != ninf && (Q8 || den[i] > 0.f) ? Mi[i] + __logf(den[i]) : ninf;
   }
 }
 
@@ -1049,12 +1064,12 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(KvArgs a, int BLK) {
   }
   for (int s0 = KR * 32; s0 < a.topk; s0 += 32) {
     const int s = s0 + lane;
-    if (s < a.topk) M = fmaxf(M, __ldg(a.part_lse + (p0 + s) * a.G + hi));
+    if (s < a.topk) M = part_max<Q8>(M, __ldg(a.part_lse + (p0 + s) * a.G + hi));
   }
 #pragma unroll
-  for (int r = 0; r < KR; ++r) M = fmaxf(M, lk[r]);
+  for (int r = 0; r < KR; ++r) M = part_max<Q8>(M, lk[r]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  for (int o = 16; o > 0; o >>= 1) M = part_max<Q8>(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;

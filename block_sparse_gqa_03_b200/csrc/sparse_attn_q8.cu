@@ -24,6 +24,8 @@
 // 4 us pass before the first block arrives, the others in the merges behind the last one.
 // A block's K scale joins the softmax scale of its scores and its V scale the fp32
 // accumulation of its product, so that neither is rounded to 16 bits.
+// A NaN among a row's visible scores makes its maximum, and with it its output and
+// log-sum-exp, NaN (a maximum that left NaN out would make a row of NaN scores look empty).
 #include <math.h>
 
 #include <type_traits>
@@ -121,12 +123,12 @@ struct WarpStateTQ {
         s[u][2] = j + 8 < lim ? s[u][2] : ninf;
         s[u][3] = j + 8 < lim ? s[u][3] : ninf;
       }
-      mx0 = fmax3(mx0, s[u][0], s[u][2]);
-      mx1 = fmax3(mx1, s[u][1], s[u][3]);
+      mx0 = fmax3_nan(mx0, s[u][0], s[u][2]);
+      mx1 = fmax3_nan(mx1, s[u][1], s[u][3]);
     }
-    mx0 = warp_max_xor(warp_max_xor(warp_max_xor(mx0, 4), 8), 16);
-    mx1 = warp_max_xor(warp_max_xor(warp_max_xor(mx1, 4), 8), 16);
-    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+    mx0 = warp_max_xor_nan(warp_max_xor_nan(warp_max_xor_nan(mx0, 4), 8), 16);
+    mx1 = warp_max_xor_nan(warp_max_xor_nan(warp_max_xor_nan(mx1, 4), 8), 16);
+    const float mn0 = fmax_nan(m0, mx0), mn1 = fmax_nan(m1, mx1);
     const float c0 = exp2_approx(m0 - mn0), c1 = exp2_approx(m1 - mn1);
     m0 = mn0;
     m1 = mn1;
@@ -271,12 +273,12 @@ struct WarpStateQ {
         sc[nt][2] = j < lim ? sc[nt][2] : ninf;
         sc[nt][3] = j + 1 < lim ? sc[nt][3] : ninf;
       }
-      mx_a = fmax3(mx_a, sc[nt][0], sc[nt][1]);
-      mx_b = fmax3(mx_b, sc[nt][2], sc[nt][3]);
+      mx_a = fmax3_nan(mx_a, sc[nt][0], sc[nt][1]);
+      mx_b = fmax3_nan(mx_b, sc[nt][2], sc[nt][3]);
     }
-    mx_a = warp_max_xor(warp_max_xor(mx_a, 1), 2);
-    mx_b = warp_max_xor(warp_max_xor(mx_b, 1), 2);
-    const float mn_a = fmaxf(m_a, mx_a), mn_b = fmaxf(m_b, mx_b);
+    mx_a = warp_max_xor_nan(warp_max_xor_nan(mx_a, 1), 2);
+    mx_b = warp_max_xor_nan(warp_max_xor_nan(mx_b, 1), 2);
+    const float mn_a = fmax_nan(m_a, mx_a), mn_b = fmax_nan(m_b, mx_b);
     const float c_a = exp2_approx(m_a - mn_a), c_b = exp2_approx(m_b - mn_b);
     m_a = mn_a;
     m_b = mn_b;
@@ -498,7 +500,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
   if (tid < a.G) {
     float M = ninf;
 #pragma unroll
-    for (int w = 0; w < NC; ++w) M = fmaxf(M, mm[w * 16 + tid]);
+    for (int w = 0; w < NC; ++w) M = fmax_nan(M, mm[w * 16 + tid]);
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < NC; ++w) {
@@ -567,7 +569,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, co
         for (int i = 0; i < U; ++i) {
           float Mn = M[i];
 #pragma unroll
-          for (int k = 0; k < K; ++k) Mn = fmaxf(Mn, l[i][k]);
+          for (int k = 0; k < K; ++k) Mn = fmax_nan(Mn, l[i][k]);
           if (Mn == ninf) continue;
           const float c = exp2f((M[i] - Mn) * kLog2e);
           M[i] = Mn;
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, NC == 2 ? 5 : 2)
     const int row = x / (D / 4), dim = (x % (D / 4)) * 4;
     float4 val;
     float lsev;
-    merge_warps4<D, NC, LD>(mo, mm, ml, a.G, row, dim, val, lsev);
+    merge_warps4<D, NC, LD, true>(mo, mm, ml, a.G, row, dim, val, lsev);
     const int hq = rg.g * a.G + row;
     store_out4(a, rg, hq, dim, val);
     if (dim == 0 && a.lse) a.lse[(int64_t)rg.bt * a.H + hq] = lsev;
