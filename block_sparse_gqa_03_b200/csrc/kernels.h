@@ -135,8 +135,8 @@ size_t kv_workspace_bytes(const Shape& s);
 int kv_launches(const Shape& s);
 cudaError_t launch_kv_attn(const Shape& s, const CUtensorMap& tmq, const CUtensorMap& tmk,
                            const CUtensorMap& tmv,
-                           const uint16_t* q, const int32_t* ids, uint16_t* out, float* lse,
-                           void* ws, size_t ws_bytes, DeviceStatus* st, cudaStream_t stream);
+                           const uint16_t* q, const void* v, const int32_t* ids, uint16_t* out,
+                           float* lse, void* ws, size_t ws_bytes, DeviceStatus* st, cudaStream_t stream);
 
 // Test hook: one bounded wait that runs out and records kErrTimeout.
 cudaError_t launch_wait_timeout_probe(DeviceStatus* st, uint64_t wait_ns, cudaStream_t stream);

@@ -926,7 +926,7 @@ cudaError_t launch_sparse_attn(const Shape& s, const uint16_t* q, const void* k,
   if (by_block) {
     CUtensorMap tmq;
     if (!make_q_group_map(&tmq, q, s)) return cudaErrorInvalidValue;
-    return launch_kv_attn(s, tmq, tmk, tmv, q, ids, out, lse, partials, partial_bytes, st, stream);
+    return launch_kv_attn(s, tmq, tmk, tmv, q, v, ids, out, lse, partials, partial_bytes, st, stream);
   }
   if (!pl.stream) {
     if (s.kv8) return run_attn_q8(s, pl, k, v, a, stream);

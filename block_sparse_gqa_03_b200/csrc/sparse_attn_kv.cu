@@ -40,6 +40,10 @@
 // (11 bits instead of 8 at no cost).  The codes of a block land in the upper half of
 // the place of their widened form, and one warp widens them from the bottom up, so that
 // it never overwrites codes it has not read: no shared memory is needed for them.
+// A NaN among V's codes must reach the queries that see its token and no others, which a
+// product with a zero probability does not keep apart: it is widened to zero and noted in
+// one word per chunk, and where that is set the merge looks up, among the codes a query
+// sees, the dims that are NaN.
 // Warp 0 does nothing else there (it walks the blocks, one ahead of the tiles), and
 // warps 2 and 3 gather Q.  A block's K scale joins the softmax scale of the tile; its V
 // scale joins the slot's weight in the merge, so that partial outputs are weighted means
@@ -110,6 +114,10 @@ struct KvArgs {
   // 8-bit cache: scales per (block, KV head), and the V scale of every valid slot's block
   const float *ks, *vs;
   float* part_vs;          // [p], written by the scatter kernel
+  // 8-bit cache: V codes, and whether a NaN was met among those the tiles read
+  const uint8_t* v;
+  int64_t v_s0, v_s1, v_s2;
+  int* v_nan;
 };
 
 __device__ __forceinline__ int visible_from_length(const KvArgs& a, int L, int t) {
@@ -313,14 +321,20 @@ struct KvSmem {
   static_assert(BYTES <= LIMIT, "shared memory");
 };
 
+// The top bit of every byte of four codes that is NaN (0x7f or 0xff).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t x) {
+  return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
 // Widens N bytes of codes that lie in the upper half of the 2 N bytes at `dst` (rows of
 // 64 codes, one 64-dim atom after the other) into 16-bit rows in the 128-byte swizzle,
 // bf16 or f16.  One warp; 16 codes per lane and step.  A step reads 512 bytes and then
 // writes 1024, its last byte never beyond the next step's codes.  Rows [r0, BLK) of each
-// atom become zeros.
+// atom become zeros, and with F16 (V) so do NaN codes; returns whether this lane met one.
 template <int BLK, uint32_t N, bool F16>
-__device__ __forceinline__ void widen_codes(uint32_t dst, int r0, int lane) {
+__device__ __forceinline__ bool widen_codes(uint32_t dst, int r0, int lane) {
   const int row = lane >> 2, c = lane & 3;
+  bool nan = false;
 #pragma unroll 2
   for (uint32_t g = 0; g < N / 512; ++g) {
     uint32_t x[4];
@@ -329,6 +343,14 @@ __device__ __forceinline__ void widen_codes(uint32_t dst, int r0, int lane) {
                  : "r"(dst + N + g * 512 + lane * 16)
                  : "memory");
     if ((int)((g * 8) % BLK) + row >= r0) x[0] = x[1] = x[2] = x[3] = 0u;
+    if constexpr (F16) {
+      const uint32_t m = nan_codes(x[0]) | nan_codes(x[1]) | nan_codes(x[2]) | nan_codes(x[3]);
+      if (m != 0u) {
+        nan = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] &= ~((nan_codes(x[i]) >> 7) * 0xffu);
+      }
+    }
     __syncwarp();
     const uint32_t out = dst + g * 1024;
 #pragma unroll
@@ -351,6 +373,7 @@ __device__ __forceinline__ void widen_codes(uint32_t dst, int r0, int lane) {
                    : "memory");
     }
   }
+  return nan;
 }
 
 // Two partial outputs: bf16, or of an 8-bit cache f16 (they are weighted means of codes,
@@ -491,7 +514,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const int rows = kv_length(a.seq_lens, w.b, a.max_kv, a.st) - w.beta * BLK;
         if (!mbar_wait_warp(b_kvland + 8 * s, (use >> 1) & 1, a.st, 0x202u, a.wait_ns)) break;
         widen_codes<BLK, RAW, false>(kd, BLK, lane);
-        widen_codes<BLK, RAW, true>(vd, rows, lane);
+        if (widen_codes<BLK, RAW, true>(vd, rows, lane)) *a.v_nan = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_kvfull + 8 * s);
@@ -892,6 +915,35 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   }
 }
 
+// The dims among the 4 N from `dim` on that are NaN in V of a token that query (b, t) selects
+// and sees for KV head g: bit 8 e + 7 of word i stands for dim + 4 i + e.  Run only where
+// the tiles met a NaN.
+template <int N>
+__device__ __forceinline__ void nan_dims(const KvArgs& a, int bt, int b, int t, int g, int dim,
+                                         int BLK, uint32_t (&m)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[i] = 0u;
+  const int lim = visible_limit(a, b, t);
+  const int32_t* ids = a.ids + ((int64_t)bt * a.h + g) * a.topk;
+#pragma unroll 1
+  for (int s = 0; s < a.topk; ++s) {
+    const int beta = __ldg(ids + s);
+    if (beta < 0 || beta >= a.nblk || (int64_t)beta * BLK >= lim) continue;
+    int64_t plane = b, row = (int64_t)beta * BLK;
+    const int rows = min(BLK, lim - beta * BLK);
+    if (a.pg.table != nullptr) {
+      plane = kv_page(a.pg, b, beta, a.st);
+      row = 0;
+      if (plane < 0) continue;
+    }
+    const uint8_t* p = a.v + plane * a.v_s0 + row * a.v_s1 + g * a.v_s2 + dim;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r, p += a.v_s1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) m[i] |= nan_codes(__ldg(reinterpret_cast<const uint32_t*>(p) + i));
+  }
+}
+
 // m[base + rl] for rl < RPI, as selects (an indexed pick would put m in local memory).
 template <int RPI>
 __device__ __forceinline__ float pick_row(const float* m, int base, int rl) {
@@ -1006,6 +1058,15 @@ __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int 
           }
         }
     }
+  }
+  if (Q8 && *a.v_nan != 0) {
+    uint32_t m[2];
+    nan_dims<2>(a, bt, b, t, g, c * 8, BLK, m);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (m[e / 4] >> (8 * (e % 4) + 7) & 1u) acc[i][e] = __int_as_float(0x7fffffff);
   }
   uint16_t* ob = a.out + (int64_t)b * a.o_s0 + (int64_t)t * a.o_s1 + c * 8;
 #pragma unroll
@@ -1129,6 +1190,14 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(KvArgs a, int BLK) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
   }
+  if (Q8 && *a.v_nan != 0) {
+    // with two dims per lane, the word that holds them
+    uint32_t m[1];
+    nan_dims<1>(a, bt, b, t, g, lane * PER / 4 * 4, BLK, m);
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+      if (m[0] >> (8 * (lane * PER % 4 + e) + 7) & 1u) acc[e] = __int_as_float(0x7fffffff);
+  }
   const float inv = den > 0.f ? 1.f / den : 0.f;
   uint16_t* o = a.out + (int64_t)b * a.o_s0 + (int64_t)t * a.o_s1 + (int64_t)hq * a.o_s2 + lane * PER;
   if constexpr (PER == 4) {
@@ -1157,6 +1226,9 @@ struct KvPlan {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// The counts, and behind those of an 8-bit cache its v_nan: cleared together.
+size_t counts_bytes(const Shape& s, const KvPlan& p) { return (size_t)(p.nj + (s.kv8 ? 1 : 0)) * 4; }
+
 KvPlan plan_kv(const Shape& s) {
   KvPlan p;
   p.rows = (int64_t)s.batch * s.n_q;
@@ -1179,7 +1251,7 @@ KvPlan plan_kv(const Shape& s) {
   p.max_tiles = (int64_t)((slots + p.qpt - 1) / p.qpt) + p.nj;
   size_t off = 0;
   p.counts_off = off;
-  off = up256(off + p.nj * 4);
+  off = up256(off + counts_bytes(s, p));
   p.offs_off = off;
   off = up256(off + (p.nj + 1) * 4);
   p.toffs_off = off;
@@ -1216,7 +1288,7 @@ cudaError_t run_kv(const Shape& s, KvArgs& a, const KvPlan& p, const CUtensorMap
   for (int c = 0; c < p.nchunks; ++c) {
     a.bt0 = (int64_t)c * p.chunk_rows;
     a.nbt = (int)((p.rows - a.bt0) < p.chunk_rows ? (p.rows - a.bt0) : p.chunk_rows);
-    err = cudaMemsetAsync(ws + p.counts_off, 0, p.nj * 4, stream);
+    err = cudaMemsetAsync(ws + p.counts_off, 0, counts_bytes(s, p), stream);
     if (err != cudaSuccess) return err;
     const int64_t n = (int64_t)a.nbt * s.h * s.topk;
     const int grid = (int)((n + 255) / 256 < (int64_t)sms * 8 ? (n + 255) / 256 : (int64_t)sms * 8);
@@ -1270,8 +1342,9 @@ int kv_launches(const Shape& s) { return 5 * plan_kv(s).nchunks; }
 
 cudaError_t launch_kv_attn(const Shape& s, const CUtensorMap& tmq, const CUtensorMap& tmk,
                            const CUtensorMap& tmv,
-                           const uint16_t* q, const int32_t* ids, uint16_t* out, float* lse,
-                           void* ws, size_t ws_bytes, DeviceStatus* st, cudaStream_t stream) {
+                           const uint16_t* q, const void* v, const int32_t* ids, uint16_t* out,
+                           float* lse, void* ws, size_t ws_bytes, DeviceStatus* st,
+                           cudaStream_t stream) {
   const KvPlan p = plan_kv(s);
   if (ws == nullptr || ws_bytes < p.total) return cudaErrorInvalidValue;
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
@@ -1313,6 +1386,11 @@ cudaError_t launch_kv_attn(const Shape& s, const CUtensorMap& tmq, const CUtenso
   a.ks = s.ks;
   a.vs = s.vs;
   a.part_vs = reinterpret_cast<float*>(w + p.vs_off);
+  a.v = static_cast<const uint8_t*>(v);
+  a.v_s0 = s.v_s[0];
+  a.v_s1 = s.v_s[1];
+  a.v_s2 = s.v_s[2];
+  a.v_nan = a.counts + p.nj;
 #define MSA_KV_CASE(D_, B_)                                                          \
   if (s.d == D_ && s.block == B_)                                                    \
     return s.kv8 ? run_kv<D_, B_, true>(s, a, p, tmq, tmk, tmv, tmo, w, stream)      \

@@ -412,7 +412,8 @@ MSA_API msa_status_t msa_index_select_q8(const msa_params_t* params, const msa_b
 /* msa_sparse_attn over the 8-bit cache: softmax attention with k = k_scale * code and
  * v = v_scale * code of the selected blocks' visible tokens; fp32 softmax and
  * accumulation, bf16 out, the same handling of ids, empty rows and lse.  A NaN in a
- * query or in a key that it sees makes the row's output and lse NaN. */
+ * query or in a key that it sees makes the row's output and lse NaN, one in V the same
+ * dim of the outputs that see its token. */
 MSA_API msa_status_t msa_sparse_attn_q8(const msa_params_t* params, const msa_bf16_t* q,
                                         const msa_e4m3_t* k, const msa_e4m3_t* v,
                                         const float* k_scale, const float* v_scale,

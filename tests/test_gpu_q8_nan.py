@@ -94,3 +94,43 @@ def test_a_visible_nan_key_or_query_makes_the_row_nan(case, paged):
         assert bool(hit.any()) == (L > 0)
         if n > 1 and 4 * topk * block < max_kv:
             assert not bool(hit.all())
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("case", CASES)
+def test_a_nan_value_reaches_the_rows_that_see_it_and_no_others(case, paged):
+    """Values behind a query's position are masked: one that is NaN must not reach it, in a
+    block that later queries see or in any other."""
+    way, n, H, h, d, block, topk, max_kv, lens = case
+    g, c, table, q, ids, run = problem(*case, paged)
+    # zeros where NaN will be: the other rows' bits are those of this cache
+    bad = torch.zeros((len(lens), max_kv, h, d), dtype=torch.bool, device=DEV)
+    spots = []
+    for b, L in enumerate(lens):
+        at = torch.randint(0, max(L, 1), (4,), device=DEV, generator=g).tolist()
+        at += [max(L - 1, 0), max(L - n, 0), max(L - 1 - n // 2, 0), 0]
+        for i, j in enumerate(at):
+            dims = torch.randint(0, d, (3,), device=DEV, generator=g)
+            dims[0] = (d - 1, 0, d // 2)[i % 3]
+            spots.append((b, j, i % h, dims, (0x7f, 0xff)[i % 2]))
+            bad[b, j, i % h, dims] = j < L
+    for b, j, head, dims, _ in spots:
+        put(c.v, table, block, b, j, head, dims, 0)
+    clean = run()
+    assert bool(torch.isfinite(clean[0]).all())
+    for b, j, head, dims, code in spots:
+        put(c.v, table, block, b, j, head, dims, code)
+    out, lse = run()
+    G = H // h
+    assert torch.equal(lse, clean[1])
+    for b, L in enumerate(lens):
+        see = visible(ids, b, L, n, h, block, max_kv)
+        hit = torch.einsum("nhj,jhd->nhd", see.float(), bad[b].float()).repeat_interleave(G, 1) > 0
+        assert bool(torch.isnan(out[b][hit]).all())
+        assert torch.equal(out[b][~hit], clean[0][b][~hit])
+        assert L == 0 or n == 1 or (bool(hit.any()) and not bool(hit.all()))
+    again = run()
+    assert torch.equal(u8(again[0]), u8(out))
+    for b, j, head, dims, _ in spots:  # and nothing of it stays in the workspace
+        put(c.v, table, block, b, j, head, dims, 0)
+    assert torch.equal(run()[0], clean[0])
