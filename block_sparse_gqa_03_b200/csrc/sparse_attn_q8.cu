@@ -486,8 +486,10 @@ template <int D, int NC, int LD, int NT, class Sync>
 __device__ __forceinline__ void finish_row(const AttnArgs& a, int c, int cur, const RowGeo& rg,
                                         float* mo, float* mm, float* ml, int* flag, int tid,
                                         Sync sync) {
-  // items per thread, and segments of each, whose loads are under way together
-  constexpr int U = NT == 32 ? 4 : 2, K = NT == 32 ? 2 : 4;
+  // items per thread, and segments of each, whose loads are under way together.  K sets the
+  // order of the roundings, so it is the same whoever merges: with 2 here and 4 there, a row
+  // of four segments and more changed its last bits with the CTA that came last.
+  constexpr int U = NT == 32 ? 4 : 2, K = 4;
   const int c_first = cur * a.topk / a.per;
   const int nseg = ((cur + 1) * a.topk - 1) / a.per - c_first + 1;
   const int seg = c - c_first;
