@@ -981,6 +981,7 @@ __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int 
   const int rl = lane / LPR, c = lane % LPR;
   const int64_t p0 = ((int64_t)bt_rel * a.h + g) * a.topk;
   const float ninf = -__int_as_float(0x7f800000);
+  const int v_nan = Q8 ? __ldg(a.v_nan) : 0;  // loaded here, its latency is hidden
   // pass 1: per-head maximum of the slots' log-sum-exps (empty or invalid slots
   // hold -inf), slots spread over the lanes; a slot's row is kept for pass 2
   float M[GC];
@@ -1059,7 +1060,7 @@ __global__ void __launch_bounds__(256, 2) kv_combine_group_kernel(KvArgs a, int 
         }
     }
   }
-  if (Q8 && *a.v_nan != 0) {
+  if (Q8 && v_nan != 0) {
     uint32_t m[2];
     nan_dims<2>(a, bt, b, t, g, c * 8, BLK, m);
 #pragma unroll
@@ -1105,6 +1106,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(KvArgs a, int BLK) {
   const int b = bt / a.n_q, t = bt % a.n_q;
   const int64_t p0 = ((int64_t)bt_rel * a.h + g) * a.topk;
   const float ninf = -__int_as_float(0x7f800000);
+  const int v_nan = Q8 ? __ldg(a.v_nan) : 0;  // loaded here, its latency is hidden
   constexpr int PER = D / 32;  // dims per lane
   // pass 1: the slots' log-sum-exps and partial rows (empty or invalid slots hold
   // -inf and row -1, written by the scatter kernel), both loaded at once; the
@@ -1190,7 +1192,7 @@ __global__ void __launch_bounds__(256) kv_combine_kernel(KvArgs a, int BLK) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
   }
-  if (Q8 && *a.v_nan != 0) {
+  if (Q8 && v_nan != 0) {
     // with two dims per lane, the word that holds them
     uint32_t m[1];
     nan_dims<1>(a, bt, b, t, g, lane * PER / 4 * 4, BLK, m);
