@@ -48,3 +48,21 @@ def test_split_rows_repeat_their_bits(H, h, d, block, topk, max_kv, lens):
         for out, lse in got[1:]:
             assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1]), draw
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n,H,h,d,block,topk,max_kv,lens", [
+    (700, 12, 2, 64, 32, 6, 900, [900, 800]),        # by row
+    (1100, 32, 4, 64, 64, 5, 1100, [1100]),          # by block, whose lists are filled by atomics
+    (1300, 10, 2, 128, 128, 6, 1400, [1400, 1301]),
+])
+def test_prompts_repeat_their_bits(n, H, h, d, block, topk, max_kv, lens):
+    g, batch = gen(n), len(lens)
+    c, _ = filled(g, batch=batch, max_kv=max_kv, h=h, d=d, block=block, paged=False, scales="free")
+    q, ids = rows(g, batch, n, H, d), pick(g, lens, n, h, -(-max_kv // block), block, topk)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want = None
+    for _ in range(60):
+        got = msa.msa_sparse_attn_q8(q, c.k, c.v, c.k_scale, c.v_scale, ids, block=block,
+                                     seq_lens=sl, return_lse=True)
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
