@@ -50,9 +50,10 @@
 // of codes and are kept in f16 (bf16 ones doubled the rounding of the output: error
 // against 64 bits 0.0024 instead of 0.0017 of its norm).
 // A 4096-query chunk of a 32K prompt (32 heads in 4 groups of 128 dims, 32 blocks of 64
-// each): 620 to 646 us, of which the index 45, the tiles 351 and the merge 222.  What
-// bounds it: the partials, 1.07 GB written at the 3.3 TB/s at which this card writes and
-// read once.  Chunks whose partials stay in L2 (60, 190, 440 MB) took 1780, 1016 and 766
+// each): 629 to 650 us, of which the index 52, the tiles 343 and the merge 229 (under ncu).
+// The 1.07 GB of partials are written and read once, which at the rates of a fill and of a
+// copy is half of that (144 and 164 us); the tiles write 3.1 TB/s, where a fill writes 7.5,
+// with the tensor pipe at 17%, so neither is what bounds them.  Chunks whose partials stay in L2 (60, 190, 440 MB) took 1780, 1016 and 766
 // us: a block then meets too few queries for full tiles, and each chunk costs five
 // launches.
 // Buffers: 2-4 Q tiles (released when S is computed), 2 K/V stages, and in tensor

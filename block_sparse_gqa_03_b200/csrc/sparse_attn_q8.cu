@@ -19,7 +19,7 @@
 //  * the merge buffer's rows are padded by 16 bytes (unpadded, four lanes met on one
 //    bank at every store).
 // Bound: HBM, 2 d bytes per selected visible token and group.  16 x 128K tokens, 64
-// heads in 8 groups of 128 dims, 128 of 2048 blocks each: 50.6 us against 41.4 us of
+// heads in 8 groups of 128 dims, 128 of 2048 blocks each: 52.1 to 52.8 us against 41.4 us of
 // HBM time (268 MB at the measured copy rate; the bf16 cache: 93 us); of the rest about
 // 4 us pass before the first block arrives, the others in the merges behind the last one.
 // A block's K scale joins the softmax scale of its scores and its V scale the fp32
