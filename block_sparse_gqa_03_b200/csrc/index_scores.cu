@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kScanWarps * 32) index_scan_kernel(ScanArgs a)
   for (int beta = wid; beta < F; beta += nw) {
     float cm[NT][2];
     block_max<DI, NT>(a, kidx_block(a, b, beta, q), L, beta, r, bq, lim, cm);
-    const float sc = a.scale != nullptr ? __ldg(a.scale + (int64_t)b * a.nblk + beta) : 1.f;
+    const float sc = a.scale != nullptr ? __ldg(a.scale + (int64_t)b * kis_stride(a.nblk) + beta) : 1.f;
     if (r == 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)

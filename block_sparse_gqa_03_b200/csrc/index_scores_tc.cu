@@ -81,6 +81,27 @@ __device__ __forceinline__ void bitonic_sort(uint32_t (&v)[N]) {
       }
 }
 
+// N consecutive block scales, N aligned.
+template <int N>
+__device__ __forceinline__ void load_scales(const float* p, float (&s)[N]) {
+  if constexpr (N == 1) {
+    s[0] = __ldg(p);
+  } else if constexpr (N == 2) {
+    const float2 x = __ldg(reinterpret_cast<const float2*>(p));
+    s[0] = x.x;
+    s[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
+      s[i] = x.x;
+      s[i + 1] = x.y;
+      s[i + 2] = x.z;
+      s[i + 3] = x.w;
+    }
+  }
+}
+
 // SCALED: the key is in units of a scale per block, which is positive and so moves out
 // of the maximum.
 template <int DI, int BLK, bool TOPK, bool SCALED>
@@ -279,11 +300,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // warp touches 32 sectors for 128 bytes (2048 queries over 32K in blocks of 16: 114 us,
     // four at a time 57 us).  With the two of a block of 64 nothing is gained.
     const bool vec = a.nblk % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scores) & 15u) == 0;
-    float held = 1.f;  // SCALED: the scale of block `lane` of the next 32
+    // SCALED: the scales of a tile's blocks, loaded a tile ahead (may be none past the
+    // sequence, and past the last tile none is used)
+    float sc[bpt], sc_next[bpt];
+    const float* scales = SCALED ? a.scale + (int64_t)b * kis_stride(a.nblk) + kt0 * bpt : nullptr;
+    if constexpr (SCALED) load_scales<bpt>(scales, sc_next);
     for (int kt = 0; kt < n_kt && ng < ng_valid; ++kt) {
       const int buf = kt & 1;
-      if (SCALED && (kt * bpt) % 32 == 0)
-        held = __ldg(a.scale + (int64_t)b * a.nblk + min((kt0 + kt) * bpt + lane, a.nblk - 1));
+      if constexpr (SCALED) {
+#pragma unroll
+        for (int k = 0; k < bpt; ++k) sc[k] = sc_next[k];
+        load_scales<bpt>(scales + (kt + 1) * bpt, sc_next);
+      }
       if (!mbar_wait_warp(b_afull + 8 * buf, (kt >> 1) & 1, a.st, 0x106u, a.wait_ns)) break;
       tc::fence_after_sync();
       const int j0 = (kt0 + kt) * kKT;
@@ -296,10 +324,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_aempty + 8 * buf);
-      float bm[bpt], sc[bpt];
-#pragma unroll
-      for (int k = 0; k < bpt; ++k)
-        sc[k] = SCALED ? __shfl_sync(0xffffffffu, held, (kt * bpt + k) & 31) : 1.f;
+      float bm[bpt];
       if (vis >= kKT) {
 #pragma unroll
         for (int k = 0; k < bpt; ++k) {

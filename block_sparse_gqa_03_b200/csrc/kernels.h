@@ -21,10 +21,14 @@ struct Shape {
   // [batch, nblk, h] or [num_pages, h]
   bool kv8;
   const float *ks, *vs;
-  // index key in units of a scale per block, dense [batch, nblk]: the block maxima of the
-  // score kernels for n_q > 1 are multiplied by it (nullptr: no scales)
+  // index key in units of a scale per block, [batch, kis_stride(nblk)]: the block maxima of
+  // the score kernels for n_q > 1 are multiplied by it (nullptr: no scales)
   const float* kis;
 };
+
+// Floats from one sequence's block scales to the next: 16-byte rows that may be read 8 past
+// the last group of 8 blocks.
+inline __host__ __device__ int kis_stride(int nblk) { return (nblk + 7) / 8 * 8 + 8; }
 
 // The tensors of an 8-bit cache: e4m3 codes with the shape's strides, and fp32
 // scales, dense [batch, nblk, h] or [num_pages, h] (K_idx: without the head axis).
@@ -96,7 +100,7 @@ cudaError_t launch_append_kv_q8(const Shape& s, const uint16_t* k_new, const uin
 
 // Rows [base, base + n) of every sequence of an 8-bit cache (those below its length)
 // as bf16, dense [batch, n, h, d] / [batch, n, d_idx].  With `block_scales` ([batch,
-// nblk], base 0) the index key comes out as codes, and the scales of its blocks there.
+// kis_stride(nblk)], base 0) the index key comes out as codes, the scales of its blocks there.
 cudaError_t launch_read_kv_q8(const Shape& s, const Q8Cache& c, int64_t base, int64_t n,
                               uint16_t* k_out, uint16_t* v_out, uint16_t* ki_out, DeviceStatus* st,
                               cudaStream_t stream, float* block_scales = nullptr);

@@ -211,8 +211,10 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
     scale_at = plane;
   }
   const bool bad = plane < 0;  // recorded by kv_page; the rows read as zeros
-  if (a.block_scales != nullptr && threadIdx.x == 0 && p0 == (int64_t)beta * a.block)
-    a.block_scales[(int64_t)b * a.nblk + beta] = bad ? 1.f : a.kis[scale_at];
+  // (loaded here and stored at the end, so that the codes' loads do not wait for it)
+  const bool first = a.block_scales != nullptr && threadIdx.x == 0 && p0 == (int64_t)beta * a.block;
+  float block_scale = 1.f;
+  if (first && !bad) block_scale = __ldg(a.kis + scale_at);
   const int rows = (int)(p1 - p0);
   const int64_t out0 = (int64_t)b * a.n + (p0 - a.base);
   // K and V: piece = (head, row, 16 codes), a head's rows together
@@ -256,6 +258,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
   plane_of(a.k, a.k_s, a.ks, a.h, a.d, a.k_out);
   plane_of(a.v, a.v_s, a.vs, a.h, a.d, a.v_out);
   plane_of(a.ki, a.ki_s, a.block_scales == nullptr ? a.kis : nullptr, 1, a.d_idx, a.ki_out);
+  if (first) a.block_scales[(int64_t)b * kis_stride(a.nblk) + beta] = block_scale;
 }
 
 Q8Args base_args(const Shape& s, const Q8Cache& c, DeviceStatus* st) {

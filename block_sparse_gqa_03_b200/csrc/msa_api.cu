@@ -227,7 +227,7 @@ size_t wide_idx_bytes(const Shape& s) {
 }
 
 size_t wide_scale_bytes(const Shape& s) {
-  return s.n_q > 1 ? (size_t)wide_sequences(s) * s.nblk * sizeof(float) : 0;
+  return s.n_q > 1 ? (size_t)wide_sequences(s) * msa::kis_stride(s.nblk) * sizeof(float) : 0;
 }
 
 int score_launches_q8(const Shape& s) {
