@@ -191,6 +191,9 @@ __device__ __forceinline__ uint32_t value2(uint32_t f16x2, float s) {
   return pack_bf16(v.x * s, v.y * s);
 }
 
+// CODES: the index key comes out as codes, with the scales of its blocks (a form of its own:
+// in one with the values, those took 47 us instead of 43 for the rows above).
+template <bool CODES>
 __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
   grid_dep_wait();
   grid_dep_launch();
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
   }
   const bool bad = plane < 0;  // recorded by kv_page; the rows read as zeros
   // (loaded here and stored at the end, so that the codes' loads do not wait for it)
-  const bool first = a.block_scales != nullptr && threadIdx.x == 0 && p0 == (int64_t)beta * a.block;
+  const bool first = CODES && threadIdx.x == 0 && p0 == (int64_t)beta * a.block;
   float block_scale = 1.f;
   if (first && !bad) block_scale = __ldg(a.kis + scale_at);
   const int rows = (int)(p1 - p0);
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
         if (!bad) {
           x[i] = ld_stream_u4(codes + plane * st[0] + (row0 + r) * st[1] +
                               (heads > 1 ? g * st[2] : 0) + c * 16);
-          if (scales != nullptr) s[i] = __ldg(scales + scale_at * heads + g);
+          if (!CODES) s[i] = __ldg(scales + scale_at * heads + g);
         }
         o[i] = out + ((out0 + r) * heads + g) * d + c * 16;
       }
@@ -255,9 +258,11 @@ __global__ void __launch_bounds__(kThreads) read_kv_q8_kernel(Q8Args a) {
       }
     }
   };
-  plane_of(a.k, a.k_s, a.ks, a.h, a.d, a.k_out);
-  plane_of(a.v, a.v_s, a.vs, a.h, a.d, a.v_out);
-  plane_of(a.ki, a.ki_s, a.block_scales == nullptr ? a.kis : nullptr, 1, a.d_idx, a.ki_out);
+  if constexpr (!CODES) {
+    plane_of(a.k, a.k_s, a.ks, a.h, a.d, a.k_out);
+    plane_of(a.v, a.v_s, a.vs, a.h, a.d, a.v_out);
+  }
+  plane_of(a.ki, a.ki_s, a.kis, 1, a.d_idx, a.ki_out);
   if (first) a.block_scales[(int64_t)b * kis_stride(a.nblk) + beta] = block_scale;
 }
 
@@ -327,7 +332,8 @@ cudaError_t launch_read_kv_q8(const Shape& s, const Q8Cache& c, int64_t base, in
   a.per_seq = (int)((base + n - 1) / a.group - base / a.group + 1);
   const int64_t grid = (int64_t)s.batch * a.per_seq;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(read_kv_q8_kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
+  return launch_pdl(block_scales == nullptr ? read_kv_q8_kernel<false> : read_kv_q8_kernel<true>,
+                    dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace msa
